@@ -32,7 +32,10 @@ EXPORTS = (
     "csa_set_wait_limit_ns", "csa_check_wait_timeout", "csa_forward_staged", "csa_decode_staged",
     "csa_project_compress_workspace_bytes", "csa_project_hidden_compress", "csa_cp_workspace_bytes",
     "csa_cp_compress", "csa_cp_queries", "csa_quantize_keys_e4m3", "csa_decode_q8", "csa_decode_q8_staged",
-    "csa_debug_build",
+    "csa_debug_build", "csa_quantize_f8", "csa_dequantize_f8", "csa_quantize_weight_f8",
+    "csa_gemm_f8_workspace_bytes", "csa_gemm_f8", "csa_mqa_f8_workspace_bytes", "csa_sparse_mqa_f8",
+    "csa_decode_mqa_f8", "csa_cache_append_f8", "csa_packed_weights_f8_bytes", "csa_pack_weights_f8",
+    "csa_decode_f8_workspace_bytes", "csa_decode_f8",
 )
 
 
@@ -80,7 +83,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{os.path.basename(LIB_PATH)} not built at {LIB_PATH}; run __graft_entry__.build()")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        vp, i, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
         D = ctypes.POINTER(csa_dims)
         sig = {
             "csa_packed_weights_bytes": (sz, [D]),
@@ -117,6 +120,19 @@ def lib() -> ctypes.CDLL:
             "csa_decode_staged": (i, [D, vp, vp, vp, vp, vp, vp, vp, i, i, vp, vp, vp, sz, vp, vp]),
             "csa_check_wait_timeout": (i, [vp, vp]),
             "csa_debug_build": (i, []),
+            "csa_quantize_f8": (i, [i, vp, ll, i, i, i, vp, i, vp, ll, vp, ll, vp]),
+            "csa_dequantize_f8": (i, [i, vp, ll, vp, ll, i, i, i, vp, i, vp, ll, vp]),
+            "csa_quantize_weight_f8": (i, [i, vp, ll, i, i, vp, ll, vp, ll, vp]),
+            "csa_gemm_f8_workspace_bytes": (sz, [i, i, i]),
+            "csa_gemm_f8": (i, [i, vp, ll, vp, ll, vp, ll, vp, ll, i, i, i, vp, ll, vp, sz, vp]),
+            "csa_mqa_f8_workspace_bytes": (sz, [D, i]),
+            "csa_sparse_mqa_f8": (i, [D, vp, i, vp, vp, vp, vp, vp, i, i, i, vp, vp, sz, vp]),
+            "csa_decode_mqa_f8": (i, [D, vp, i, vp, vp, vp, vp, i, i, vp, vp, sz, vp]),
+            "csa_cache_append_f8": (i, [D, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, vp]),
+            "csa_packed_weights_f8_bytes": (sz, [D]),
+            "csa_pack_weights_f8": (i, [D, vp, vp, sz, vp]),
+            "csa_decode_f8_workspace_bytes": (sz, [D, i, i]),
+            "csa_decode_f8": (i, [D, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -360,3 +376,85 @@ def csa_decode_q8_staged(dims: Dims, packed, h, pos, ring, Ccache, KIcodes, KIsc
                                       _p(KIscale), _p(cache_len), cap, B, _p(O), _p(idx_out), _p(ws),
                                       ws.numel() * ws.element_size(), _event_array(events), _stream(stream)),
            "csa_decode_q8_staged")
+
+
+# ---------------------------------------------------------------- block-scaled 8-bit rows
+
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def csa_quantize_f8(dtype, X, ld, n, w, block, slots, n_slots, codes, ld_codes, scales, ld_scales, stream=None):
+    """n rows of w values to E4M3 codes and scale bytes, row i into row slots[i] (None: i)."""
+    _check(lib().csa_quantize_f8(dtype, _p(X), ld, n, w, block, _p(slots), n_slots, _p(codes), ld_codes, _p(scales),
+                                 ld_scales, _stream(stream)), "csa_quantize_f8")
+
+
+def csa_dequantize_f8(dtype, codes, ld_codes, scales, ld_scales, n_slots, w, block, rows, n, X, ld, stream=None):
+    """Rows rows[i] (None: i) of a block-scaled cache back to values of dtype."""
+    _check(lib().csa_dequantize_f8(dtype, _p(codes), ld_codes, _p(scales), ld_scales, n_slots, w, block, _p(rows), n,
+                                   _p(X), ld, _stream(stream)), "csa_dequantize_f8")
+
+
+def csa_quantize_weight_f8(dtype, W, ld, N, K, codes, ld_codes, scales, ld_scales, stream=None):
+    """W [N, K] to codes and one scale byte for each 128 x 128 values."""
+    _check(lib().csa_quantize_weight_f8(dtype, _p(W), ld, N, K, _p(codes), ld_codes, _p(scales), ld_scales,
+                                        _stream(stream)), "csa_quantize_weight_f8")
+
+
+def csa_gemm_f8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib().csa_gemm_f8_workspace_bytes(M, N, K)
+
+
+def csa_gemm_f8(out_dtype, A, lda, sA, ld_sA, B, ldb, sB, ld_sB, M, N, K, D, ldd, ws=None, stream=None):
+    """D [M, N] = A . B^T of two block-scaled matrices."""
+    _check(lib().csa_gemm_f8(out_dtype, _p(A), lda, _p(sA), ld_sA, _p(B), ldb, _p(sB), ld_sB, M, N, K, _p(D), ldd,
+                             _p(ws), _bytes(ws), _stream(stream)), "csa_gemm_f8")
+
+
+def csa_mqa_f8_workspace_bytes(dims: Dims, rows: int) -> int:
+    return lib().csa_mqa_f8_workspace_bytes(_d(dims), rows)
+
+
+def csa_sparse_mqa_f8(dims: Dims, q, ld_q, codes, scales, idx, cu_seqlens, cu_blocks, nseq, total_tokens,
+                      total_blocks, O, ws=None, stream=None):
+    """csa_sparse_mqa over 8-bit entries."""
+    _check(lib().csa_sparse_mqa_f8(_d(dims), _p(q), ld_q, _p(codes), _p(scales), _p(idx), _p(cu_seqlens),
+                                   _p(cu_blocks), nseq, total_tokens, total_blocks, _p(O), _p(ws), _bytes(ws),
+                                   _stream(stream)), "csa_sparse_mqa_f8")
+
+
+def csa_decode_mqa_f8(dims: Dims, q, ld_q, codes, scales, idx, pos, cap, B, O, ws=None, stream=None):
+    """The same for decode rows over [B, cap] caches."""
+    _check(lib().csa_decode_mqa_f8(_d(dims), _p(q), ld_q, _p(codes), _p(scales), _p(idx), _p(pos), cap, B, _p(O),
+                                   _p(ws), _bytes(ws), _stream(stream)), "csa_decode_mqa_f8")
+
+
+def csa_cache_append_f8(dims: Dims, packed, rows, pos, ring, Ccodes, Cscale, KIcodes, KIscale, cache_len, cap, B,
+                        stream=None):
+    """csa_cache_append with both caches in 8 bits."""
+    _check(lib().csa_cache_append_f8(_d(dims), _p(packed), _p(rows), _p(pos), _p(ring), _p(Ccodes), _p(Cscale),
+                                     _p(KIcodes), _p(KIscale), _p(cache_len), cap, B, _stream(stream)),
+           "csa_cache_append_f8")
+
+
+def csa_packed_weights_f8_bytes(dims: Dims) -> int:
+    return lib().csa_packed_weights_f8_bytes(_d(dims))
+
+
+def csa_pack_weights_f8(dims: Dims, packed, packed_f8, stream=None):
+    """The projection weights of `packed` as 8-bit operands."""
+    _check(lib().csa_pack_weights_f8(_d(dims), _p(packed), _p(packed_f8), _bytes(packed_f8), _stream(stream)),
+           "csa_pack_weights_f8")
+
+
+def csa_decode_f8_workspace_bytes(dims: Dims, B: int, cap: int) -> int:
+    return lib().csa_decode_f8_workspace_bytes(_d(dims), B, cap)
+
+
+def csa_decode_f8(dims: Dims, packed, packed_f8, h, pos, ring, Ccodes, Cscale, KIcodes, KIscale, cache_len, cap, B, O,
+                  idx_out=None, ws=None, stream=None):
+    """One decode step with 8-bit projections over 8-bit caches."""
+    _check(lib().csa_decode_f8(_d(dims), _p(packed), _p(packed_f8), _p(h), _p(pos), _p(ring), _p(Ccodes), _p(Cscale),
+                               _p(KIcodes), _p(KIscale), _p(cache_len), cap, B, _p(O), _p(idx_out), _p(ws),
+                               _bytes(ws), _stream(stream)), "csa_decode_f8")

@@ -18,6 +18,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "f8_rows.cuh"
 
 namespace csa {
 
@@ -210,6 +211,8 @@ struct AppendArgs {
   int c, cI, cap, ring_w;
   uint8_t* KIcodes;     // quantised key cache (Q8): [B, cap, cI] E4M3 codes
   float* KIscale;       // [B, cap] scales
+  uint8_t* Ccodes;      // quantised entry cache (C8): [B, cap, c] E4M3 codes
+  uint8_t* Cscale;      // [B, cap] scale bytes
   int wait_late;        // 1: the previous kernel on the stream reads and writes none of the above
                         // and was scheduled after everything before it had completed (decode:
                         // the c^Q-side projection), so the append runs beside it and waits for it
@@ -219,9 +222,10 @@ struct AppendArgs {
 // One CTA per sequence: store the token's row in ring slot t mod 2m, then, if
 // t closes block i = (t+1)/m - 1, compress that block from the ring.  Q8:
 // the indexer-key entry goes to an E4M3 cache (its bf16 value quantised with
-// one scale, max |v| / 448) instead of a bf16 one.
-template <typename T, int M, bool Q8>
-__device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_s) {
+// one scale, max |v| / 448) instead of a bf16 one.  C8: the KV entry, rounded
+// to T likewise, goes to a cache of block-scaled E4M3 rows (one scale byte).
+template <typename T, int M, bool Q8, bool C8>
+__device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_s, T* c_s) {
   const int b = blockIdx.x;
   const int t = a.pos[b];
   if (t < 0) {
@@ -267,7 +271,8 @@ __device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_
       }
     }
     const float v = compress_channel<M>(la, lb, ca, cb, has_prev);
-    if (main) static_cast<T*>(a.Ccache)[((long long)b * a.cap + i) * c + ch] = from_f32<T>(v);
+    if (main && C8) c_s[ch] = from_f32<T>(v);
+    else if (main) static_cast<T*>(a.Ccache)[((long long)b * a.cap + i) * c + ch] = from_f32<T>(v);
     else if (Q8) ki_s[ch] = to_f32(from_f32<T>(v));   // the entry as stored in T, then quantised below
     else static_cast<T*>(a.KIcache)[((long long)b * a.cap + i) * cI + ch] = from_f32<T>(v);
   }
@@ -285,16 +290,39 @@ __device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_
       if (threadIdx.x == 0) a.KIscale[(long long)b * a.cap + i] = scale;
     }
   }
+  if constexpr (C8) {
+    if (threadIdx.x >= 32 && threadIdx.x < 64) {   // beside the key entry's warp
+      const int lane = threadIdx.x & 31, units = c / f8::kUnit;   // c <= 1024: at most two units per lane
+      f8::Unit<T> x[2];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (lane + 32 * k < units) x[k].load_shared(c_s + (lane + 32 * k) * f8::kUnit);
+        else x[k].clear();
+        top = max(top, x[k].amax());
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int sb = f8::scale_byte(top);
+      const float inv = f8::inv_scale(sb);
+      const long long e = (long long)b * a.cap + i;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < units)
+          *reinterpret_cast<uint4*>(a.Ccodes + e * c + (lane + 32 * k) * f8::kUnit) = x[k].encode(inv);
+      if (lane == 0) a.Cscale[e] = (uint8_t)sb;
+    }
+  }
   if (threadIdx.x == 0) a.cache_len[b] = i + 1;
 }
 
 // With a.wait_late the wait for the previous kernel comes after the append's
 // own work, so the kernel after it sees both complete.
-template <typename T, int M, bool Q8 = false>
+template <typename T, int M, bool Q8 = false, bool C8 = false>
 __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a) {
   __shared__ float ki_s[1024];
+  __shared__ __align__(16) T c_s[C8 ? 1024 : 8];
   if (!a.wait_late) pdl_prologue_done();
-  cache_append_cta<T, M, Q8>(a, ki_s);
+  cache_append_cta<T, M, Q8, C8>(a, ki_s, c_s);
   if (a.wait_late) pdl_prologue_done();
 }
 

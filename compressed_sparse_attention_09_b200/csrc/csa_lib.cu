@@ -16,10 +16,14 @@
 #include "common.cuh"
 #include "compress.cuh"
 #include "decode_q8.cuh"
+#include "f8_rows.cuh"
+#include "gemm_f8_tcgen05.cuh"
 #include "gemm_simt.cuh"
 #include "gemm_tcgen05.cuh"
 #include "indexer_simt.cuh"
 #include "indexer_tcgen05.cuh"
+#include "mqa_f8_simt.cuh"
+#include "mqa_f8_tcgen05.cuh"
 #include "mqa_simt.cuh"
 #include "mqa_tcgen05.cuh"
 #include "pack.cuh"
@@ -1172,7 +1176,7 @@ namespace {
 csa_status launch_append(const csa_dims* d, const void* packed, const void* rows, long long ld_rows,
                          const int* pos, void* ring, void* Ccache, void* KIcache, int* cache_len, int cap,
                          int B, cudaStream_t st, uint8_t* KIcodes = nullptr, float* KIscale = nullptr,
-                         bool wait_late = false) {
+                         bool wait_late = false, uint8_t* Ccodes = nullptr, uint8_t* Cscale = nullptr) {
   CSA_RANGE("A6 cache_append");
   if (B == 0) return CSA_OK;
   const bool q8 = KIcodes != nullptr;
@@ -1186,10 +1190,12 @@ csa_status launch_append(const csa_dims* d, const void* packed, const void* rows
   a.BbI = reinterpret_cast<const float*>(at((void*)packed, P.bbI));
   a.c = d->c; a.cI = d->cI; a.cap = cap; a.ring_w = 4 * d->c + 4 * d->cI;
   a.KIcodes = KIcodes; a.KIscale = KIscale;
+  a.Ccodes = Ccodes; a.Cscale = Cscale;
   a.wait_late = wait_late ? 1 : 0;
 #define CSA_APPEND_CASE(MM)                                                                    \
   case MM: {                                                                                   \
-    const cudaError_t e_ = q8 ? launch_pdl(cache_append_kernel<bf16, MM, true>, dim3(B), dim3(256), 0, st, a) \
+    const cudaError_t e_ = Ccodes ? launch_pdl(cache_append_kernel<bf16, MM, true, true>, dim3(B), dim3(256), 0, st, a) \
+                         : q8 ? launch_pdl(cache_append_kernel<bf16, MM, true>, dim3(B), dim3(256), 0, st, a) \
                          : d->dtype == CSA_BF16                                                \
                              ? launch_pdl(cache_append_kernel<bf16, MM>, dim3(B), dim3(256), 0, st, a)       \
                              : launch_pdl(cache_append_kernel<float, MM>, dim3(B), dim3(256), 0, st, a);     \
@@ -1437,6 +1443,514 @@ csa_status csa_decode_q8_staged(const csa_dims* d, const void* packed, const voi
     if (!events[i]) return CSA_ERR_INVALID_ARG;
   return decode_impl(d, packed, h, pos, ring, Ccache, nullptr, cache_len, cap, B, O, idx_out, ws, ws_bytes, events,
                      stream, static_cast<uint8_t*>(KIcodes), KIscale);
+}
+
+}  // extern "C"
+
+// ====================================================================== block-scaled E4M3 rows
+namespace {
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t st) {
+  CSA_RANGE("quantize_f8");
+  if (a.n == 0) return CSA_OK;
+  const bool b = dtype == CSA_BF16;
+  if (block != f8::kBlock) {   // one scale a row: a warp each
+    const unsigned grid = (unsigned)(((long long)a.n * 32 + 255) / 256);
+    const cudaError_t e = b ? launch_pdl(f8::quantize_rows_kernel<bf16>, dim3(grid), dim3(256), 0, st, a)
+                            : launch_pdl(f8::quantize_rows_kernel<float>, dim3(grid), dim3(256), 0, st, a);
+    if (e != cudaSuccess) return CSA_ERR_CUDA;
+    CSA_CHECK_LAUNCH();
+    return CSA_OK;
+  }
+  // threads are numbered in 32 bits: more than that many in several launches
+  const long long per = 8ll * ((a.w + f8::kBlock - 1) / f8::kBlock);
+  const int step = (int)std::max(1ll, std::min<long long>(a.n, (1ll << 30) / per));
+  for (int r = 0; r < a.n; r += step) {
+    a.row0 = r;
+    const unsigned units = (unsigned)(per * std::min(step, a.n - r)), grid = (units + 255) / 256;
+    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, dim3(grid), dim3(256), 0, st, a, units)
+                            : launch_pdl(f8::quantize_blocks_kernel<float>, dim3(grid), dim3(256), 0, st, a, units);
+    if (e != cudaSuccess) return CSA_ERR_CUDA;
+    CSA_CHECK_LAUNCH();
+    if (a.n - r <= step) break;
+  }
+  return CSA_OK;
+}
+
+csa_status launch_quantize_squares(int dtype, const void* W, long long ld, int N, int K, void* codes,
+                                   long long ld_codes, void* scales, long long ld_scales, cudaStream_t st) {
+  const dim3 grid((unsigned)((K + f8::kBlock - 1) / f8::kBlock),
+                  (unsigned)std::min((N + f8::kBlock - 1) / f8::kBlock, 65535));
+  const cudaError_t e =
+      dtype == CSA_BF16
+          ? launch_pdl(f8::quantize_squares_kernel<bf16>, grid, dim3(256), 0, st, static_cast<const bf16*>(W), ld, N, K,
+                       static_cast<uint8_t*>(codes), ld_codes, static_cast<uint8_t*>(scales), ld_scales)
+          : launch_pdl(f8::quantize_squares_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(W), ld, N,
+                       K, static_cast<uint8_t*>(codes), ld_codes, static_cast<uint8_t*>(scales), ld_scales);
+  if (e != cudaSuccess) return CSA_ERR_CUDA;
+  CSA_CHECK_LAUNCH();
+  return CSA_OK;
+}
+
+template <int BN, int kStages>
+csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8GemmArgs& a, cudaStream_t st) {
+  using Cfg = F8GemmCfg<BN, kStages>;
+  auto k = gemm_f8_kernel<BN, kStages>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  const TcGemmArgs& g = a.g;
+  const int tiles = ((g.M + Cfg::BM - 1) / Cfg::BM) * ((g.N + BN - 1) / BN) * g.k_split;
+  const int grid = tiles < sm_count() ? tiles : sm_count();
+  if (launch_pdl(k, dim3(grid), dim3(224), Cfg::SMEM, st, ta, tb, a) != cudaSuccess) return CSA_ERR_CUDA;
+  CSA_CHECK_LAUNCH();
+  if (g.k_split > 1) {
+    const int m_pad = ((g.M + Cfg::BM - 1) / Cfg::BM) * Cfg::BM;
+    const long long n = (long long)g.N * g.M;
+    if (launch_pdl(gemm_split_reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g.part, g.k_split,
+                   g.M, m_pad, g.N, g.out) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    CSA_CHECK_LAUNCH();
+  }
+  return CSA_OK;
+}
+
+// K slices of a product with few rows (weights as the 128-row operand): as
+// many as fill the SMs, each at least two K blocks.
+int f8_gemm_splits(int M, int N, int K) {
+  if (M > 64) return 1;
+  const int w_tiles = (N + 127) / 128, k_blocks = (K + 127) / 128;
+  for (int ks = 8; ks >= 2; ks /= 2)
+    if ((long long)w_tiles * ks <= sm_count() && k_blocks % ks == 0 && k_blocks / ks >= 2) return ks;
+  return 1;
+}
+size_t f8_gemm_ws(int M, int N, int K) {
+  const int ks = f8_gemm_splits(M, N, K);
+  return ks > 1 ? (size_t)ks * (size_t)round_up_int(N, 128) * (size_t)M * 4 : 0;
+}
+
+// D[M, N] = A . B^T over block-scaled rows, routed to `out` (see launch_gemm
+// for the two operand orders).  sa: one byte per row of A and K block; sb: one
+// per 128 rows of B.
+csa_status launch_gemm_f8(const void* A, long long lda, const void* sa, long long ld_sa, const void* B, long long ldb,
+                          const void* sb, long long ld_sb, int M, int N, int K, const GemmOut& out, void* ws,
+                          cudaStream_t st) {
+  CSA_RANGE("gemm_f8");
+  if (M == 0 || N == 0) return CSA_OK;
+  CUtensorMap ta, tb;
+  F8GemmArgs a;
+  a.g.K = K;
+  a.g.out = out;
+  a.g.k_split = 1;
+  a.g.part = nullptr;
+  const ScaleRows rows_a{static_cast<const uint8_t*>(sa), ld_sa, 1, M};
+  const ScaleRows rows_b{static_cast<const uint8_t*>(sb), ld_sb, f8::kBlock, N};
+  if (M <= 64) {   // few rows: the weights fill the 128-row operand, the epilogue transposes
+    if (!make_tmap_u8(&ta, B, K, N, (uint64_t)ldb, 128, 128) || !make_tmap_u8(&tb, A, K, M, (uint64_t)lda, 128, 64))
+      return CSA_ERR_UNSUPPORTED;
+    a.g.M = N; a.g.N = M; a.g.transpose_out = 1;
+    a.g.group_m = (N + 127) / 128;
+    a.sa = rows_b;
+    a.sb = rows_a;
+    a.g.k_split = f8_gemm_splits(M, N, K);
+    a.g.part = static_cast<float*>(ws);
+    return launch_f8_gemm<64, 8>(ta, tb, a, st);
+  }
+  a.g.M = M; a.g.N = N; a.g.transpose_out = 0;
+  a.sa = rows_a;
+  a.sb = rows_b;
+  const int m_tiles = (M + 127) / 128;
+  auto cost = [&](int bn) {   // waves of tiles times a tile's length
+    const long long tiles = (long long)m_tiles * ((N + bn - 1) / bn), sms = sm_count();
+    return (double)((tiles + sms - 1) / sms) * (double)bn;
+  };
+  const int BN = cost(128) < cost(192) ? 128 : 192;
+  if (!make_tmap_u8(&ta, A, K, M, (uint64_t)lda, 128, 128) || !make_tmap_u8(&tb, B, K, N, (uint64_t)ldb, 128, BN))
+    return CSA_ERR_UNSUPPORTED;
+  const int n_tiles = (N + BN - 1) / BN, sq = std::max(1, (int)lrint(sqrt((double)sm_count())));
+  a.g.group_m = (size_t)M * K > ((size_t)32 << 20) ? std::max(sq, (sm_count() + n_tiles - 1) / n_tiles) : m_tiles;
+  if (a.g.group_m > m_tiles) a.g.group_m = m_tiles;
+  return BN == 192 ? launch_f8_gemm<192, 5>(ta, tb, a, st) : launch_f8_gemm<128, 6>(ta, tb, a, st);
+}
+
+// Whether the tensor-core MQA over 8-bit entries covers these dims.
+bool mqa_f8_tc_ok(const csa_dims* d) {
+  return d->dtype == CSA_BF16 && d->c == mqaf8::kC && d->nh % mqaf8::kHeads == 0;
+}
+
+// Work items per (row, head group): rows that leave SMs idle are split over
+// their tiles of 128 entries.
+int mqa_f8_splits(const csa_dims* d, int rows, int* tiles_per_split) {
+  const int tiles = (d->topk + mqaf8::kTile - 1) / mqaf8::kTile;
+  const long long items = (long long)rows * (d->nh / mqaf8::kHeads);
+  int n = items > 0 ? (int)std::min<long long>(tiles, std::max(1ll, sm_count() / items)) : 1;
+  *tiles_per_split = (tiles + n - 1) / n;
+  return (tiles + *tiles_per_split - 1) / *tiles_per_split;
+}
+size_t mqa_f8_ws(const csa_dims* d, int rows) {
+  if (!mqa_f8_tc_ok(d)) return 0;
+  int tps;
+  const int n = mqa_f8_splits(d, rows, &tps);
+  if (n <= 1) return 0;
+  const size_t rhs = (size_t)rows * d->nh * n;
+  return align_up(rhs * mqaf8::kC * 4) + align_up(rhs * 4);
+}
+
+template <typename T, int VEC>
+csa_status mqa_f8_simt_launch(const MqaF8Args& a, cudaStream_t st) {
+  if (launch_pdl(mqa_f8_simt_kernel<T, VEC>, dim3(a.rows), dim3(256), 0, st, a) != cudaSuccess) return CSA_ERR_CUDA;
+  CSA_CHECK_LAUNCH();
+  return CSA_OK;
+}
+
+csa_status launch_mqa_f8(const csa_dims* d, const MqaF8Args& a, void* ws, cudaStream_t st) {
+  CSA_RANGE("sparse_mqa_f8");
+  if (a.rows == 0) return CSA_OK;
+  if (mqa_f8_tc_ok(d)) {
+    MqaF8TcArgs t;
+    t.q = static_cast<const bf16*>(a.q); t.ld_q = a.ld_q; t.codes = a.codes; t.scales = a.scales; t.idx = a.idx;
+    t.O = static_cast<bf16*>(a.O); t.ld_O = a.ld_O; t.topk = a.topk; t.nh = a.nh; t.rows = a.rows;
+    t.scale_log2 = a.scale_log2; t.rm = a.rm;
+    t.splits = mqa_f8_splits(d, a.rows, &t.tiles_per_split);
+    const size_t rhs = (size_t)a.rows * a.nh * t.splits;
+    t.part_o = static_cast<float*>(ws);
+    t.part_lse = t.splits > 1 ? reinterpret_cast<float*>(at(ws, align_up(rhs * mqaf8::kC * 4))) : nullptr;
+    if (cudaFuncSetAttribute(mqa_f8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mqaf8::kSmem) !=
+        cudaSuccess)
+      return CSA_ERR_CUDA;
+    const long long items = (long long)a.rows * (a.nh / mqaf8::kHeads) * t.splits;
+    if (items > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
+    const int grid = items < sm_count() ? (int)items : sm_count();
+    if (launch_pdl(mqa_f8_tc_kernel, dim3(grid), dim3(mqaf8::kThreads), mqaf8::kSmem, st, t) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    CSA_CHECK_LAUNCH();
+    if (t.splits > 1) {
+      if (launch_pdl(mqa_f8_join_kernel, dim3((unsigned)(a.rows * a.nh)), dim3(128), 0, st, (const float*)t.part_o,
+                     (const float*)t.part_lse, a.nh, t.splits, t.O, t.ld_O) != cudaSuccess)
+        return CSA_ERR_CUDA;
+      CSA_CHECK_LAUNCH();
+    }
+    return CSA_OK;
+  }
+  const bool b = d->dtype == CSA_BF16;
+  switch (d->c / 32) {
+    case 2: return b ? mqa_f8_simt_launch<bf16, 2>(a, st) : mqa_f8_simt_launch<float, 2>(a, st);
+    case 4: return b ? mqa_f8_simt_launch<bf16, 4>(a, st) : mqa_f8_simt_launch<float, 4>(a, st);
+    case 8: return b ? mqa_f8_simt_launch<bf16, 8>(a, st) : mqa_f8_simt_launch<float, 8>(a, st);
+    case 16: return b ? mqa_f8_simt_launch<bf16, 16>(a, st) : mqa_f8_simt_launch<float, 16>(a, st);
+    case 32: return b ? mqa_f8_simt_launch<bf16, 32>(a, st) : mqa_f8_simt_launch<float, 32>(a, st);
+  }
+  return CSA_ERR_UNSUPPORTED;
+}
+
+MqaF8Args mqa_f8_args(const csa_dims* d, const void* q, long long ld_q, const void* codes, const void* scales,
+                      const int* idx, int rows, void* O) {
+  MqaF8Args a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.ld_q = ld_q; a.codes = static_cast<const uint8_t*>(codes); a.scales = static_cast<const uint8_t*>(scales);
+  a.idx = idx; a.O = O; a.ld_O = (long long)d->nh * d->c; a.topk = d->topk; a.nh = d->nh; a.rows = rows;
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d->c));
+  return a;
+}
+
+// Argument checks that the two MQA entries share.
+csa_status check_mqa_f8(const csa_dims* d, const void* q, int ld_q, const void* codes, const void* scales,
+                        const int* idx, int rows, const void* O, const void* ws, size_t ws_bytes) {
+  csa_status s = check_dims(d);
+  if (s != CSA_OK) return s;
+  if (!q || !codes || !scales || !idx || !O || rows < 0 || ld_q < d->nh * d->c) return CSA_ERR_INVALID_ARG;
+  if (ld_q % (16 / (int)elem_size(d)) || !aligned16(q) || !aligned16(codes) || !aligned16(O)) return CSA_ERR_UNSUPPORTED;
+  const size_t need = mqa_f8_ws(d, rows);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return CSA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % kPtrAlign) return CSA_ERR_INVALID_ARG;
+  }
+  return CSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+csa_status csa_quantize_f8(int dtype, const void* X, long long ld, int n, int w, int block, const int* slots,
+                           int n_slots, void* codes, long long ld_codes, void* scales, long long ld_scales,
+                           void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (!X || !codes || !scales || n < 0 || w <= 0 || ld < w || ld_codes < w || (slots && n_slots < 0))
+    return CSA_ERR_INVALID_ARG;
+  if (block != 0 && block != f8::kBlock) return CSA_ERR_UNSUPPORTED;
+  if (ld_scales < (block ? (w + block - 1) / block : 1)) return CSA_ERR_INVALID_ARG;
+  const int v = dtype == CSA_BF16 ? 8 : 4;
+  if (w % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(X) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
+  f8::QuantArgs a;
+  a.X = X; a.ld = ld; a.slots = slots; a.n_slots = n_slots; a.codes = static_cast<uint8_t*>(codes);
+  a.ld_codes = ld_codes; a.scales = static_cast<uint8_t*>(scales); a.ld_scales = ld_scales; a.n = n; a.w = w;
+  a.row0 = 0;
+  return launch_quantize(dtype, a, block, (cudaStream_t)stream);
+}
+
+csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, const void* scales, long long ld_scales,
+                             int n_slots, int w, int block, const int* rows, int n, void* X, long long ld,
+                             void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (!X || !codes || !scales || n < 0 || w <= 0 || ld < w || ld_codes < w || n_slots < 0 || (!rows && n > n_slots))
+    return CSA_ERR_INVALID_ARG;
+  if (block != 0 && block != f8::kBlock) return CSA_ERR_UNSUPPORTED;
+  if (ld_scales < (block ? (w + block - 1) / block : 1)) return CSA_ERR_INVALID_ARG;
+  const int v = dtype == CSA_BF16 ? 8 : 4;
+  if (w % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(X) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
+  if (n == 0) return CSA_OK;
+  f8::DequantArgs a;
+  a.codes = static_cast<const uint8_t*>(codes); a.ld_codes = ld_codes; a.scales = static_cast<const uint8_t*>(scales);
+  a.ld_scales = ld_scales; a.rows = rows; a.n_slots = n_slots; a.X = X; a.ld = ld; a.w = w;
+  a.block_units = (block ? block : w) / f8::kUnit;
+  // threads are numbered in 32 bits: more than that many in several launches
+  const long long per = w / f8::kUnit;
+  const int step = (int)std::max(1ll, std::min<long long>(n, (1ll << 30) / per));
+  for (int r = 0; r < n; r += step) {
+    a.row0 = r;
+    const unsigned units = (unsigned)(per * std::min(step, n - r)), grid = (units + 255) / 256;
+    const cudaError_t e =
+        dtype == CSA_BF16
+            ? launch_pdl(f8::dequantize_kernel<bf16>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, units)
+            : launch_pdl(f8::dequantize_kernel<float>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, units);
+    if (e != cudaSuccess) return CSA_ERR_CUDA;
+    CSA_CHECK_LAUNCH();
+    if (n - r <= step) break;
+  }
+  return CSA_OK;
+}
+
+csa_status csa_quantize_weight_f8(int dtype, const void* W, long long ld, int N, int K, void* codes,
+                                  long long ld_codes, void* scales, long long ld_scales, void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (!W || !codes || !scales || N <= 0 || K <= 0 || ld < K || ld_codes < K ||
+      ld_scales < (K + f8::kBlock - 1) / f8::kBlock)
+    return CSA_ERR_INVALID_ARG;
+  const int v = dtype == CSA_BF16 ? 8 : 4;
+  if (K % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(W) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
+  return launch_quantize_squares(dtype, W, ld, N, K, codes, ld_codes, scales, ld_scales, (cudaStream_t)stream);
+}
+
+size_t csa_gemm_f8_workspace_bytes(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return align_up(f8_gemm_ws(M, N, K));
+}
+
+csa_status csa_gemm_f8(int out_dtype, const void* A, long long lda, const void* sA, long long ld_sA, const void* B,
+                       long long ldb, const void* sB, long long ld_sB, int M, int N, int K, void* D, long long ldd,
+                       void* ws, size_t ws_bytes, void* stream) {
+  if (out_dtype != CSA_F32 && out_dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (!A || !sA || !B || !sB || !D || M < 0 || N <= 0 || K <= 0) return CSA_ERR_INVALID_ARG;
+  const int kb = (K + f8::kBlock - 1) / f8::kBlock;
+  if (lda < K || ldb < K || ldd < N || ld_sA < kb || ld_sB < kb) return CSA_ERR_INVALID_ARG;
+  if (lda % 16 || ldb % 16 || !aligned16(A) || !aligned16(B)) return CSA_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(D) % (out_dtype == CSA_F32 ? 4 : 2)) return CSA_ERR_INVALID_ARG;
+  if (M == 0) return CSA_OK;
+  if ((long long)((M + 127) / 128) * ((N + 127) / 128) > 0x3FFFFFFF) return CSA_ERR_UNSUPPORTED;
+  const size_t need = f8_gemm_ws(M, N, K);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return CSA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % kPtrAlign) return CSA_ERR_INVALID_ARG;
+  }
+  GemmOut o;
+  memset(&o, 0, sizeof(o));
+  o.seg[0] = {0, N, D, ldd, out_dtype == CSA_F32 ? 1 : 0};
+  o.nseg = 1;
+  return launch_gemm_f8(A, lda, sA, ld_sA, B, ldb, sB, ld_sB, M, N, K, o, ws, (cudaStream_t)stream);
+}
+
+size_t csa_mqa_f8_workspace_bytes(const csa_dims* d, int rows) {
+  if (check_dims(d) != CSA_OK || rows < 0) return 0;
+  return mqa_f8_ws(d, rows);
+}
+
+csa_status csa_sparse_mqa_f8(const csa_dims* d, const void* q, int ld_q, const void* codes, const void* scales,
+                             const int* idx, const int* cu_seqlens, const int* cu_blocks, int nseq, int total_tokens,
+                             int total_blocks, void* O, void* ws, size_t ws_bytes, void* stream) {
+  csa_status s = check_mqa_f8(d, q, ld_q, codes, scales, idx, total_tokens, O, ws, ws_bytes);
+  if (s != CSA_OK) return s;
+  if (!cu_seqlens || !cu_blocks || nseq <= 0 || total_blocks < 0) return CSA_ERR_INVALID_ARG;
+  MqaF8Args a = mqa_f8_args(d, q, ld_q, codes, scales, idx, total_tokens, O);
+  a.rm = RowMap{cu_seqlens, cu_blocks, nseq, total_blocks, nullptr, 0, d->m};
+  return launch_mqa_f8(d, a, ws, (cudaStream_t)stream);
+}
+
+csa_status csa_decode_mqa_f8(const csa_dims* d, const void* q, int ld_q, const void* codes, const void* scales,
+                             const int* idx, const int* pos, int cap, int B, void* O, void* ws, size_t ws_bytes,
+                             void* stream) {
+  csa_status s = check_mqa_f8(d, q, ld_q, codes, scales, idx, B, O, ws, ws_bytes);
+  if (s != CSA_OK) return s;
+  if (!pos || cap <= 0) return CSA_ERR_INVALID_ARG;
+  MqaF8Args a = mqa_f8_args(d, q, ld_q, codes, scales, idx, B, O);
+  a.rm = RowMap{nullptr, nullptr, 0, 0, pos, cap, d->m};
+  return launch_mqa_f8(d, a, ws, (cudaStream_t)stream);
+}
+
+csa_status csa_cache_append_f8(const csa_dims* d, const void* packed, const void* rows, const int* pos, void* ring,
+                               void* Ccodes, void* Cscale, void* KIcodes, float* KIscale, int* cache_len, int cap,
+                               int B, void* stream) {
+  csa_status s = check_dims(d);
+  if (s != CSA_OK) return s;
+  if (!packed || !rows || !pos || !ring || !Ccodes || !Cscale || !KIcodes || !KIscale || !cache_len)
+    return CSA_ERR_INVALID_ARG;
+  if (cap <= 0 || B < 0) return CSA_ERR_INVALID_ARG;
+  if (d->dtype != CSA_BF16 || !aligned16(Ccodes)) return CSA_ERR_UNSUPPORTED;
+  return launch_append(d, packed, rows, 4 * d->c + 4 * d->cI, pos, ring, nullptr, nullptr, cache_len, cap, B,
+                       (cudaStream_t)stream, static_cast<uint8_t*>(KIcodes), KIscale, false,
+                       static_cast<uint8_t*>(Ccodes), static_cast<uint8_t*>(Cscale));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- decode step in 8 bits
+namespace {
+
+// Packed 8-bit weights: the two projection matrices of csa_pack_weights as
+// E4M3 codes with a scale byte for 128 x 128 values.
+struct PackF8Layout {
+  int kb1, kb2;              // scale bytes per 128 rows
+  size_t w1, s1, w2, s2, total;
+};
+PackF8Layout pack_f8_layout(const csa_dims* d) {
+  const PackLayout P = pack_layout(d);
+  PackF8Layout L;
+  L.kb1 = round_up_int((d->d + 127) / 128, 4);
+  L.kb2 = round_up_int((d->dc + 127) / 128, 4);
+  size_t off = 0;
+  L.w1 = off; off = align_up(off + (size_t)P.N1 * d->d);
+  L.s1 = off; off = align_up(off + (size_t)((P.N1 + 127) / 128) * L.kb1);
+  L.w2 = off; off = align_up(off + (size_t)P.N2 * d->dc);
+  L.s2 = off; off = align_up(off + (size_t)((P.N2 + 127) / 128) * L.kb2);
+  L.total = off;
+  return L;
+}
+
+// The 8-bit decode step's requirements: those of the quantised key cache, and
+// whole 16-value units of the hidden row and of c^Q.
+bool f8_decode_ok(const csa_dims* d) { return q8_ok(d) && d->d % 16 == 0 && d->dc % 16 == 0; }
+
+struct DecF8Layout {
+  size_t base, xq, xs, cq, cs, gemm, mqa, total;   // base: dec_layout
+};
+DecF8Layout dec_f8_layout(const csa_dims* d, int B, int cap) {
+  const PackLayout P = pack_layout(d);
+  const PackF8Layout F = pack_f8_layout(d);
+  DecF8Layout L;
+  size_t off = 0;
+  L.base = off; off = align_up(off + dec_layout(d, B, cap).total);
+  L.xq = off; off = align_up(off + (size_t)B * d->d);
+  L.xs = off; off = align_up(off + (size_t)B * F.kb1);
+  L.cq = off; off = align_up(off + (size_t)B * d->dc);
+  L.cs = off; off = align_up(off + (size_t)B * F.kb2);
+  L.gemm = off; off = align_up(off + std::max(f8_gemm_ws(B, P.N1, d->d), f8_gemm_ws(B, P.N2, d->dc)));
+  L.mqa = off; off = align_up(off + mqa_f8_ws(d, B));
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t csa_packed_weights_f8_bytes(const csa_dims* d) {
+  if (check_dims(d) != CSA_OK || d->dtype != CSA_BF16 || d->d % 16 || d->dc % 16) return 0;
+  return pack_f8_layout(d).total;
+}
+
+csa_status csa_pack_weights_f8(const csa_dims* d, const void* packed, void* packed_f8, size_t packed_f8_bytes,
+                               void* stream) {
+  csa_status s = check_dims(d);
+  if (s != CSA_OK) return s;
+  if (!packed || !packed_f8) return CSA_ERR_INVALID_ARG;
+  if (d->dtype != CSA_BF16 || d->d % 16 || d->dc % 16) return CSA_ERR_UNSUPPORTED;
+  const PackLayout P = pack_layout(d);
+  const PackF8Layout F = pack_f8_layout(d);
+  if (packed_f8_bytes < F.total) return CSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(packed) % kPtrAlign || reinterpret_cast<uintptr_t>(packed_f8) % kPtrAlign)
+    return CSA_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  s = launch_quantize_squares(CSA_BF16, at((void*)packed, P.w1), d->d, P.N1, d->d, at(packed_f8, F.w1), d->d,
+                              at(packed_f8, F.s1), F.kb1, st);
+  if (s != CSA_OK) return s;
+  return launch_quantize_squares(CSA_BF16, at((void*)packed, P.w2), d->dc, P.N2, d->dc, at(packed_f8, F.w2), d->dc,
+                                 at(packed_f8, F.s2), F.kb2, st);
+}
+
+size_t csa_decode_f8_workspace_bytes(const csa_dims* d, int B, int cap) {
+  if (check_dims(d) != CSA_OK || B < 0 || cap <= 0 || !f8_decode_ok(d)) return 0;
+  return dec_f8_layout(d, B, cap).total;
+}
+
+csa_status csa_decode_f8(const csa_dims* d, const void* packed, const void* packed_f8, const void* h, const int* pos,
+                         void* ring, void* Ccodes, void* Cscale, void* KIcodes, float* KIscale, int* cache_len,
+                         int cap, int B, void* O, int* idx_out, void* ws, size_t ws_bytes, void* stream) {
+  CSA_RANGE("csa_decode_f8");
+  csa_status s = check_dims(d);
+  if (s != CSA_OK) return s;
+  if (!packed || !packed_f8 || !h || !pos || !ring || !Ccodes || !Cscale || !KIcodes || !KIscale || !cache_len || !O ||
+      !ws)
+    return CSA_ERR_INVALID_ARG;
+  if (cap <= 0 || B < 0) return CSA_ERR_INVALID_ARG;
+  if (!f8_decode_ok(d) || !aligned16(KIcodes) || !aligned16(Ccodes) || !aligned16(h) || !aligned16(O))
+    return CSA_ERR_UNSUPPORTED;
+  for (const void* p : {packed, packed_f8, (const void*)ws})
+    if (reinterpret_cast<uintptr_t>(p) % kPtrAlign) return CSA_ERR_INVALID_ARG;
+  const DecF8Layout W = dec_f8_layout(d, B, cap);
+  if (ws_bytes < W.total) return CSA_ERR_WORKSPACE;
+  if (B == 0) return CSA_OK;
+  const DecLayout L = dec_layout(d, B, cap);
+  const PackLayout P = pack_layout(d);
+  const PackF8Layout F = pack_f8_layout(d);
+  cudaStream_t st = (cudaStream_t)stream;
+  const int c = d->c, cI = d->cI;
+  void* base = at(ws, W.base);
+  char* y1 = at(base, L.y1);
+  float* wI = reinterpret_cast<float*>(at(base, L.wI));
+  char* y2 = at(base, L.y2);
+  int* idx = idx_out ? idx_out : reinterpret_cast<int*>(at(base, L.idx));
+  auto quantize = [&](const void* X, long long ld, int w, void* codes, void* scales, int ld_scales) {
+    f8::QuantArgs a;
+    memset(&a, 0, sizeof(a));
+    a.X = X; a.ld = ld; a.codes = static_cast<uint8_t*>(codes); a.ld_codes = w;
+    a.scales = static_cast<uint8_t*>(scales); a.ld_scales = ld_scales; a.n = B; a.w = w;
+    return launch_quantize(CSA_BF16, a, f8::kBlock, st);
+  };
+  // A1: eqs. (1), (2), (5), (7) over the quantised hidden row
+  if ((s = quantize(h, d->d, d->d, at(ws, W.xq), at(ws, W.xs), F.kb1)) != CSA_OK) return s;
+  GemmOut o;
+  memset(&o, 0, sizeof(o));
+  o.seg[0] = {0, P.N1b, y1, P.N1b, 0};
+  o.seg[1] = {P.N1b, d->nhI, wI, d->nhI, 1};
+  o.nseg = 2;
+  s = launch_gemm_f8(at(ws, W.xq), d->d, at(ws, W.xs), F.kb1, at((void*)packed_f8, F.w1), d->d,
+                     at((void*)packed_f8, F.s1), F.kb1, B, P.N1, d->d, o, at(ws, W.gemm), st);
+  if (s != CSA_OK) return s;
+  // A2: eqs. (6), (10) over the quantised c^Q
+  const char* cq = y1 + (size_t)(4 * c + 4 * cI) * 2;
+  if ((s = quantize(cq, P.N1b, d->dc, at(ws, W.cq), at(ws, W.cs), F.kb2)) != CSA_OK) return s;
+  memset(&o, 0, sizeof(o));
+  o.seg[0] = {0, P.N2, y2, P.N2, 0};
+  o.nseg = 1;
+  s = launch_gemm_f8(at(ws, W.cq), d->dc, at(ws, W.cs), F.kb2, at((void*)packed_f8, F.w2), d->dc,
+                     at((void*)packed_f8, F.s2), F.kb2, B, P.N2, d->dc, o, at(ws, W.gemm), st);
+  if (s != CSA_OK) return s;
+  // the append runs beside the c^Q-side projection, as in csa_decode
+  s = launch_append(d, packed, y1, P.N1b, pos, ring, nullptr, nullptr, cache_len, cap, B, st,
+                    static_cast<uint8_t*>(KIcodes), KIscale, /*wait_late=*/true, static_cast<uint8_t*>(Ccodes),
+                    static_cast<uint8_t*>(Cscale));
+  if (s != CSA_OK) return s;
+  IndexerArgs ia;
+  ia.qI = y2; ia.ld_qI = P.N2; ia.wI = wI; ia.ld_wI = d->nhI; ia.KI = KIcodes; ia.idx = idx;
+  ia.topk = d->topk; ia.nhI = d->nhI; ia.sc_cap = cap;
+  ia.rm = RowMap{nullptr, nullptr, 0, 0, pos, cap, d->m};
+  s = launch_indexer_decode_q8(d, ia, static_cast<uint8_t*>(KIcodes), KIscale, B, cap,
+                               reinterpret_cast<float*>(at(base, L.scratch)), at(base, L.qf16), st);
+  if (s != CSA_OK) return s;
+  MqaF8Args ma = mqa_f8_args(d, y2 + (size_t)d->nhI * cI * 2, P.N2, Ccodes, Cscale, idx, B, O);
+  ma.rm = RowMap{nullptr, nullptr, 0, 0, pos, cap, d->m};
+  return launch_mqa_f8(d, ma, at(ws, W.mqa), st);
 }
 
 }  // extern "C"

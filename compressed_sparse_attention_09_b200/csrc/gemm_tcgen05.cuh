@@ -114,6 +114,89 @@ __device__ __forceinline__ int staged_segment(const GemmOut& o, int c0, int N) {
   return -1;
 }
 
+constexpr int kGemmRows = 128;   // rows of a tile (the MMA's M)
+
+// Stores 64 accumulator columns (c0 .. c0 + 63 of row tile mt; this thread:
+// lane quarter `sub`, row = lane) of a work unit: an epilogue warp's step,
+// all 32 lanes.  `stage_out` is the warp's 32 staging rows of 128 bytes.
+// Where the 64 columns go to one bf16 segment, each thread converts its row
+// into the staging rows and the warp writes them out as whole 128-byte rows,
+// four rows per store instruction; other columns (fp32 segments, ragged
+// edges, the transposed decode form) are stored per thread.
+__device__ __forceinline__ void gemm_store_cols64(const TcGemmArgs& g, int m_tiles, int mt, int sub, int ks, int c0,
+                                                  const float* v0, const float* v1, uint8_t* stage_out) {
+  const int lane = threadIdx.x & 31;
+  const int r = mt * kGemmRows + sub * 32 + lane;
+  if (g.k_split > 1) {   // this K slice's fp32 sum, column c0 + j of row r at part[(ks N + c0 + j) Mpad + r]
+    if (r < g.M) {
+      float* dst = g.part + (size_t)ks * g.N * ((size_t)m_tiles * kGemmRows) + r;
+      const size_t ld = (size_t)m_tiles * kGemmRows;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (c0 + j < g.N) dst[(size_t)(c0 + j) * ld] = v0[j];
+        if (c0 + 32 + j < g.N) dst[(size_t)(c0 + 32 + j) * ld] = v1[j];
+      }
+    }
+    return;
+  }
+  if (g.transpose_out) {
+    // D[r][c0 + j] goes to output row c0 + j, column r: one segment
+    // per thread (its column), consecutive lanes write consecutive
+    // columns of the same output row
+    if (r < g.M) {
+      int sidx = -1;
+#pragma unroll
+      for (int s = 0; s < kMaxSeg; ++s)
+        if (s < g.out.nseg && r >= g.out.seg[s].col0 && r < g.out.seg[s].col0 + g.out.seg[s].ncols) sidx = s;
+      if (sidx >= 0) {
+        const OutSeg& sg = g.out.seg[sidx];
+        const long long col = r - sg.col0;
+        if (sg.f32) {
+          float* dst = static_cast<float*>(sg.ptr) + col;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c0 + j < g.N) dst[(long long)(c0 + j) * sg.ld] = v0[j];
+            if (c0 + 32 + j < g.N) dst[(long long)(c0 + 32 + j) * sg.ld] = v1[j];
+          }
+        } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sg.ptr) + col;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c0 + j < g.N) dst[(long long)(c0 + j) * sg.ld] = __float2bfloat16_rn(v0[j]);
+            if (c0 + 32 + j < g.N) dst[(long long)(c0 + 32 + j) * sg.ld] = __float2bfloat16_rn(v1[j]);
+          }
+        }
+      }
+    }
+    return;
+  }
+  const int sidx = staged_segment(g.out, c0, g.N);
+  if (sidx < 0) {
+    if (r < g.M && c0 < g.N) store_chunk32<__nv_bfloat16>(g.out, r, c0, g.N, v0);
+    if (r < g.M && c0 + 32 < g.N) store_chunk32<__nv_bfloat16>(g.out, r, c0 + 32, g.N, v1);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float* vv = u < 4 ? v0 : v1;
+    Vec16<__nv_bfloat16> pk;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pk.e[e] = __float2bfloat16_rn(vv[8 * (u & 3) + e]);
+    *reinterpret_cast<uint4*>(stage_out + r_sw128(lane, u)) = pk.u;
+  }
+  __syncwarp();
+  const OutSeg& sg = g.out.seg[sidx];
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sg.ptr) + (c0 - sg.col0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = 4 * i + (lane >> 3), u = lane & 7;
+    const long long row = (long long)mt * kGemmRows + sub * 32 + rr;
+    const uint4 val = *reinterpret_cast<const uint4*>(stage_out + r_sw128(rr, u));
+    if (row < g.M) *reinterpret_cast<uint4*>(dst + row * sg.ld + 8 * u) = val;
+  }
+  __syncwarp();
+}
+
 template <int BN, int kStages>
 __global__ void __launch_bounds__(192, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, TcGemmArgs g) {
@@ -204,11 +287,7 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
   } else {  // ---------------- epilogue warps 2..5
-    // 64 columns per TMEM wait.  Where the 64 columns go to one bf16 segment,
-    // each thread converts its row into this warp's 32 staging rows (row =
-    // lane) and the warp writes them out as whole 128-byte rows, four rows
-    // per store instruction; other columns (fp32 w^I, ragged edges, the
-    // transposed decode form) are stored per thread.
+    // 64 columns per TMEM wait
     const int sub = warp & 3;   // TMEM lane quarter this warp may access
     uint8_t* stage_out = smOut + (warp - 2) * (32 * 128);
     int acc = 0;
@@ -219,81 +298,13 @@ __global__ void __launch_bounds__(192, 1)
       gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
       if (!mbar_wait(&tfull[acc], acc_phase)) { *abort_flag = 1; break; }
       tc_fence_after();
-      const int r = mt * Cfg::BM + sub * 32 + lane;
 #pragma unroll 1
       for (int ch = 0; ch < BN / 64; ++ch) {
         float v0[32], v1[32];
         const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * BN + ch * 64);
         tmem_ld_32x32b_x32_pair(ta, ta + 32u, v0, v1);
         const int c0 = nt * BN + ch * 64;
-        if (g.k_split > 1) {   // this K slice's fp32 sum, column c0 + j of row r at part[(ks N + c0 + j) Mpad + r]
-          if (r < g.M) {
-            float* dst = g.part + (size_t)ks * g.N * ((size_t)m_tiles * Cfg::BM) + r;
-            const size_t ld = (size_t)m_tiles * Cfg::BM;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (c0 + j < g.N) dst[(size_t)(c0 + j) * ld] = v0[j];
-              if (c0 + 32 + j < g.N) dst[(size_t)(c0 + 32 + j) * ld] = v1[j];
-            }
-          }
-          continue;
-        }
-        if (g.transpose_out) {
-          // D[r][c0 + j] goes to output row c0 + j, column r: one segment
-          // per thread (its column), consecutive lanes write consecutive
-          // columns of the same output row
-          if (r < g.M) {
-            int sidx = -1;
-#pragma unroll
-            for (int s = 0; s < kMaxSeg; ++s)
-              if (s < g.out.nseg && r >= g.out.seg[s].col0 && r < g.out.seg[s].col0 + g.out.seg[s].ncols) sidx = s;
-            if (sidx >= 0) {
-              const OutSeg& sg = g.out.seg[sidx];
-              const long long col = r - sg.col0;
-              if (sg.f32) {
-                float* dst = static_cast<float*>(sg.ptr) + col;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  if (c0 + j < g.N) dst[(long long)(c0 + j) * sg.ld] = v0[j];
-                  if (c0 + 32 + j < g.N) dst[(long long)(c0 + 32 + j) * sg.ld] = v1[j];
-                }
-              } else {
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sg.ptr) + col;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  if (c0 + j < g.N) dst[(long long)(c0 + j) * sg.ld] = __float2bfloat16_rn(v0[j]);
-                  if (c0 + 32 + j < g.N) dst[(long long)(c0 + 32 + j) * sg.ld] = __float2bfloat16_rn(v1[j]);
-                }
-              }
-            }
-          }
-          continue;
-        }
-        const int sidx = staged_segment(g.out, c0, g.N);
-        if (sidx < 0) {
-          if (r < g.M && c0 < g.N) store_chunk32<__nv_bfloat16>(g.out, r, c0, g.N, v0);
-          if (r < g.M && c0 + 32 < g.N) store_chunk32<__nv_bfloat16>(g.out, r, c0 + 32, g.N, v1);
-          continue;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* vv = u < 4 ? v0 : v1;
-          Vec16<__nv_bfloat16> pk;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pk.e[e] = __float2bfloat16_rn(vv[8 * (u & 3) + e]);
-          *reinterpret_cast<uint4*>(stage_out + r_sw128(lane, u)) = pk.u;
-        }
-        __syncwarp();
-        const OutSeg& sg = g.out.seg[sidx];
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sg.ptr) + (c0 - sg.col0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3), u = lane & 7;
-          const long long row = (long long)mt * Cfg::BM + sub * 32 + rr;
-          const uint4 val = *reinterpret_cast<const uint4*>(stage_out + r_sw128(rr, u));
-          if (row < g.M) *reinterpret_cast<uint4*>(dst + row * sg.ld + 8 * u) = val;
-        }
-        __syncwarp();
+        gemm_store_cols64(g, m_tiles, mt, sub, ks, c0, v0, v1, stage_out);
       }
       tc_fence_before();
       __syncwarp();

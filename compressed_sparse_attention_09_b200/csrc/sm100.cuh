@@ -288,6 +288,57 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- 8-bit MMA
+// D[tmem] (+)= A[smem] . B[smem]^T, 8-bit floating-point inputs (K = 32), fp32
+// accumulation.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 A/B, fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same product with block scales: each operand row has one UE8M0 byte
+// (2^(b - 127)) for the K = 32 values of the instruction, held in TMEM (row r
+// of the operand in lane r % 32, column r / 32; byte `sf_id` of the 32-bit
+// cell, chosen in the instruction descriptor).
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t sfa_tmem, uint32_t sfb_tmem) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// Instruction descriptor of kind::mxf8f6f4 with E4M3 A/B, UE8M0 scales (both
+// operands' from byte `sf_id` of their cells), both K-major.
+__host__ __device__ constexpr uint32_t idesc_mxe4m3(int M, int N, int sf_id) {
+  return ((uint32_t)sf_id << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+         ((uint32_t)sf_id << 29);
+}
+
+// Copy 32 rows of 16 bytes (512 contiguous bytes of shared memory) to four
+// TMEM columns, the same 32 lanes' worth in every lane quarter: the scale
+// bytes of 128 operand rows (row 32 j + i in word j of the i-th 16 bytes).
+// Ordered before the MMAs the same thread issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
+  const uint64_t desc = (uint64_t)((smem_addr >> 4) & 0x3FFFu)   // start address / 16
+                        | ((uint64_t)(128 >> 4) << 32)            // 8-row groups 128 B apart
+                        | ((uint64_t)1 << 46);                    // descriptor version; no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // ---------------------------------------------------------------- cp.async (16 B, zero-filled when src_bytes = 0)
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)

@@ -446,6 +446,123 @@ csa_status csa_decode_q8_staged(const csa_dims* dims, const void* packed, const 
                                 void* const* events, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Block-scaled 8-bit rows (E4M3)                                          */
+/* ---------------------------------------------------------------------- */
+/* A format of this library (the page fixes no precision): a row of w values
+ * is w E4M3 codes (one byte each) and one scale byte for each block of the
+ * row, the block being 128 values (`block` = 128; the last block of a row may
+ * be shorter) or the whole row (`block` = 0).  A code c under scale byte b
+ * stands for c * 2^(b - 127).  For a block whose largest finite magnitude is
+ * A, b is the smallest byte with A <= 448 * 2^(b - 127) (0 when A = 0), and
+ * code = E4M3(x * 2^(127 - b)) to nearest even.  An infinite or NaN value is
+ * stored as the NaN code and does not enter A.  Decoding is exact in fp32 and
+ * (but for overflow and subnormals) in bf16.
+ *
+ * Cache entries use block = 0: codes [B * cap, c] and one byte per entry.
+ * The operands of the 8-bit product use block = 128, its weights one byte for
+ * 128 x 128 values. */
+
+/* Quantises n rows of w values as they are written to a cache (or to an
+ * operand of csa_gemm_f8).
+ * dtype             : CSA_BF16 or CSA_F32, the type of X.
+ * X [dev]           : rows of w values, row stride ld (elements).
+ * slots [dev, opt.] : [n] int32, the destination row of each row; NULL: row i
+ *                     goes to row i.  -1 skips the row; any other value outside
+ *                     [0, n_slots) skips it and flags CSA_ERR_BAD_INDEX.  Rows
+ *                     that no slot names keep their contents.  Two rows with
+ *                     the same slot leave that slot's contents undefined.
+ * n_slots           : destination rows (used with slots only).
+ * codes, scales [dev]: destination, row strides ld_codes, ld_scales (bytes).
+ * Requires w, ld_codes multiples of 16, rows of X and codes 16-byte aligned
+ * (CSA_ERR_UNSUPPORTED). */
+csa_status csa_quantize_f8(int dtype, const void* X, long long ld, int n, int w, int block, const int* slots,
+                           int n_slots, void* codes, long long ld_codes, void* scales, long long ld_scales,
+                           void* stream);
+
+/* Reads n rows back: row i of X is row rows[i] of the cache (NULL: row i,
+ * n <= n_slots), decoded and rounded to dtype.  rows[i] = -1 gives zeros; any
+ * other value outside [0, n_slots) gives zeros and flags CSA_ERR_BAD_INDEX.
+ * Alignment as for csa_quantize_f8. */
+csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, const void* scales,
+                             long long ld_scales, int n_slots, int w, int block, const int* rows, int n, void* X,
+                             long long ld, void* stream);
+
+/* Quantises a K-major weight matrix W [N, K] (row stride ld) with one scale
+ * byte for each 128 x 128 values (edges shorter): codes [N, ld_codes], scales
+ * [ceil(N / 128), ld_scales].  Alignment as for csa_quantize_f8 (K for w). */
+csa_status csa_quantize_weight_f8(int dtype, const void* W, long long ld, int N, int K, void* codes,
+                                  long long ld_codes, void* scales, long long ld_scales, void* stream);
+
+/* Workspace bytes of csa_gemm_f8 (0 where it needs none). */
+size_t csa_gemm_f8_workspace_bytes(int M, int N, int K);
+
+/* D[M, N] = A . B^T of two block-scaled matrices, accumulated in fp32 and
+ * rounded once to out_dtype (CSA_BF16 or CSA_F32):
+ *   D[i, j] = sum_b 2^(sA[i, b] + sB[j / 128, b] - 254) sum_{k in block b} A[i, k] B[j, k]
+ * A [dev] : [M, K] codes, row stride lda (bytes); sA [M, ld_sA] scale bytes
+ *           (csa_quantize_f8 with block = 128).
+ * B [dev] : [N, K] codes, row stride ldb; sB [ceil(N / 128), ld_sB]
+ *           (csa_quantize_weight_f8).
+ * D [dev] : row stride ldd (elements).
+ * Any M >= 0, N, K >= 1; lda and ldb multiples of 16 and A, B 16-byte aligned
+ * (CSA_ERR_UNSUPPORTED).
+ * ws [dev]: >= csa_gemm_f8_workspace_bytes(M, N, K), 256-byte aligned; may be
+ *           NULL where that is 0.  Calls that overlap need their own. */
+csa_status csa_gemm_f8(int out_dtype, const void* A, long long lda, const void* sA, long long ld_sA, const void* B,
+                       long long ldb, const void* sB, long long ld_sB, int M, int N, int K, void* D, long long ldd,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of csa_sparse_mqa_f8 and csa_decode_mqa_f8 for this many
+ * query rows (0 where they need none). */
+size_t csa_mqa_f8_workspace_bytes(const csa_dims* dims, int rows);
+
+/* csa_sparse_mqa (eq. 11) over 8-bit entries: codes [total_blocks, c] and
+ * scales [total_blocks] (block = 0) replace Ccomp; everything else is as
+ * there.  q and O are of dims.dtype, 16-byte aligned, and q's row stride a
+ * multiple of 16 bytes (CSA_ERR_UNSUPPORTED).  A row whose slots are all -1
+ * gives zeros.
+ * ws [dev]: >= csa_mqa_f8_workspace_bytes(dims, total_tokens), 256-byte
+ *           aligned; may be NULL where that is 0.  Calls that overlap need
+ *           their own. */
+csa_status csa_sparse_mqa_f8(const csa_dims* dims, const void* q, int ld_q, const void* codes, const void* scales,
+                             const int* idx, const int* cu_seqlens, const int* cu_blocks, int nseq,
+                             int total_tokens, int total_blocks, void* O, void* ws, size_t ws_bytes, void* stream);
+
+/* The same for decode rows: row b is the token at pos[b] [dev] of sequence b
+ * and sees entries s < floor(pos[b] / m) of its cache, codes [B, cap, c] and
+ * scales [B, cap].  Workspace: csa_mqa_f8_workspace_bytes(dims, B). */
+csa_status csa_decode_mqa_f8(const csa_dims* dims, const void* q, int ld_q, const void* codes, const void* scales,
+                             const int* idx, const int* pos, int cap, int B, void* O, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* csa_cache_append with both caches in 8 bits: the KV entry of a block that
+ * closes is rounded to bf16 and quantised into Ccodes [B, cap, c] and Cscale
+ * [B, cap] (block = 0), the key entry into the format of csa_decode_q8.
+ * bf16 dims, Ccodes 16-byte aligned (CSA_ERR_UNSUPPORTED otherwise). */
+csa_status csa_cache_append_f8(const csa_dims* dims, const void* packed, const void* rows, const int* pos,
+                               void* ring, void* Ccodes, void* Cscale, void* KIcodes, float* KIscale,
+                               int* cache_len, int cap, int B, void* stream);
+
+/* The projection weights of `packed` (csa_pack_weights) as 8-bit operands.
+ * packed_f8 [dev]: csa_packed_weights_f8_bytes(dims) bytes, 256-byte aligned.
+ * bf16 dims with d and dc multiples of 16 (the size is 0 otherwise). */
+size_t csa_packed_weights_f8_bytes(const csa_dims* dims);
+csa_status csa_pack_weights_f8(const csa_dims* dims, const void* packed, void* packed_f8, size_t packed_f8_bytes,
+                               void* stream);
+
+/* One decode step in 8 bits: csa_decode_q8 with the projections as
+ * csa_gemm_f8 of the quantised hidden row and c^Q (block = 128) and
+ * packed_f8, and with the KV entries in 8 bits as well.  `packed` supplies
+ * the position biases of the append.  Dims as for csa_decode_q8 and
+ * csa_pack_weights_f8; h, Ccodes, KIcodes and O 16-byte aligned.
+ * ws [dev]: >= csa_decode_f8_workspace_bytes(dims, B, cap), 256-byte aligned. */
+size_t csa_decode_f8_workspace_bytes(const csa_dims* dims, int B, int cap);
+csa_status csa_decode_f8(const csa_dims* dims, const void* packed, const void* packed_f8, const void* h,
+                         const int* pos, void* ring, void* Ccodes, void* Cscale, void* KIcodes, float* KIscale,
+                         int* cache_len, int cap, int B, void* O, int* idx_out, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Status                                                                  */
 /* ---------------------------------------------------------------------- */
 
