@@ -1580,18 +1580,18 @@ bool mqa_f8_tc_ok(const csa_dims* d) {
 }
 
 // Work items per (row, head group): rows that leave SMs idle are split over
-// their tiles of 128 entries.
-int mqa_f8_splits(const csa_dims* d, int rows, int* tiles_per_split) {
-  const int tiles = (d->topk + mqaf8::kTile - 1) / mqaf8::kTile;
+// their parts of 64 entries.
+int mqa_f8_splits(const csa_dims* d, int rows, int* parts_per_split) {
+  const int parts = (d->topk + mqaf8::kPart - 1) / mqaf8::kPart;
   const long long items = (long long)rows * (d->nh / mqaf8::kHeads);
-  int n = items > 0 ? (int)std::min<long long>(tiles, std::max(1ll, sm_count() / items)) : 1;
-  *tiles_per_split = (tiles + n - 1) / n;
-  return (tiles + *tiles_per_split - 1) / *tiles_per_split;
+  const int n = items > 0 ? (int)std::min<long long>(parts, std::max(1ll, sm_count() / items)) : 1;
+  *parts_per_split = (parts + n - 1) / n;
+  return (parts + *parts_per_split - 1) / *parts_per_split;
 }
 size_t mqa_f8_ws(const csa_dims* d, int rows) {
   if (!mqa_f8_tc_ok(d)) return 0;
-  int tps;
-  const int n = mqa_f8_splits(d, rows, &tps);
+  int per;
+  const int n = mqa_f8_splits(d, rows, &per);
   if (n <= 1) return 0;
   const size_t rhs = (size_t)rows * d->nh * n;
   return align_up(rhs * mqaf8::kC * 4) + align_up(rhs * 4);
@@ -1612,7 +1612,7 @@ csa_status launch_mqa_f8(const csa_dims* d, const MqaF8Args& a, void* ws, cudaSt
     t.q = static_cast<const bf16*>(a.q); t.ld_q = a.ld_q; t.codes = a.codes; t.scales = a.scales; t.idx = a.idx;
     t.O = static_cast<bf16*>(a.O); t.ld_O = a.ld_O; t.topk = a.topk; t.nh = a.nh; t.rows = a.rows;
     t.scale_log2 = a.scale_log2; t.rm = a.rm;
-    t.splits = mqa_f8_splits(d, a.rows, &t.tiles_per_split);
+    t.splits = mqa_f8_splits(d, a.rows, &t.parts_per_split);
     const size_t rhs = (size_t)a.rows * a.nh * t.splits;
     t.part_o = static_cast<float*>(ws);
     t.part_lse = t.splits > 1 ? reinterpret_cast<float*>(at(ws, align_up(rhs * mqaf8::kC * 4))) : nullptr;

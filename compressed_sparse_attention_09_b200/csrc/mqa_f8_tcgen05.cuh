@@ -6,42 +6,47 @@
 // tensor cores as they are: no widening pass, half the shared memory and half
 // the gather of a bf16 tile.  The other operand keeps its precision by being
 // split into two E4M3 parts:
-//   q = 2^k (hi + lo / 32)   per head, k from the row's maximum: a bf16 value
-//                            has 8 significant bits, hi takes the upper 4 and
-//                            lo the rest, so the split is exact (down to
-//                            2^-22 of the row's largest value);
-//   w = hi + lo              the softmax weight times the entry's scale: about
-//                            8 bits (its rounding error, rms 0.06 %, is below
-//                            that of a bf16 weight, 0.11 %).
-// A work item is one query row and 64 of its heads (and a range of its tiles
-// where rows are few).  Per tile of 128 selected entries
-//   S[128, 128] = [hi; lo] . C^T    M = 128 (64 heads x hi, lo), N = 128
-//                                   entries, K = 512: 16 MMAs, the full rate
-//                                   that 64 heads alone (M = 64) cannot reach
-//   s = scale_q scale_e (S_hi + S_lo / 32), w = 2^(s + e - M) on the fly
-//   O[64, 512] += w_hi . C + w_lo . C    M = 64, N = 2 x 256 channels, K = 128
-// where 2^e is the entry's scale (a power of two: it moves into the exponent)
-// and M the running maximum of s + e, so that the weights use E4M3's range
-// whatever the entries' scales are.  The normaliser is summed in fp32 from
-// the unrounded probabilities.
+//   q = 2^k (hi + lo)   per head, k from the row's maximum: a bf16 value has 8
+//                       significant bits, hi (E4M3) takes the upper 4 and lo
+//                       (E4M3) the rest, so the split is exact but for values
+//                       below 2^-9 of the row's largest (2^-17 of it off);
+//   w = hi + lo         the softmax weight times the entry's scale: hi E4M3,
+//                       lo E5M2, whose range keeps small weights at 3 bits.
+//                       Rounding within 2^-7 (rms 0.12 %, as a bf16 weight).
+// A work item is one query row and 64 of its heads (and a range of its parts
+// where rows are few).  Per part of 64 selected entries
+//   S[128, 64] = [hi; lo] . C^T     M = 128 (64 heads x hi, lo), N = 64
+//                                   entries, K = 512: 16 MMAs
+//   s = scale_q scale_e (S_hi + S_lo), p = 2^(s - R), u = p scale_e
+//   O[64, 512] += w_hi . C + w_lo . C    M = 64, N = 2 x 256 channels, K = 64;
+//                                   w = u 2^(R - M + kOff)
+// with R a lane's running maximum of s and M the head's (lagging) running
+// maximum of s + log2(scale_e), so that the weights use E4M3's range whatever
+// the entries' scales are.  The normaliser is summed in fp32 from the
+// unrounded probabilities.
 //
 // The codes sit in shared memory once, [4 chunks of 128 channels][256 ring
-// entries][128 bytes] in the 128-byte swizzle: S reads 128 entries as a
+// entries][128 bytes] in the 128-byte swizzle: S reads 64 entries as a
 // K-major operand, O reads the same bytes MN-major (32 entries = K, 256
-// channels = N, two chunks apart by the ring's length).  The ring is filled
-// and released in parts of 64 entries and read by S in tiles of 128.
+// channels = N, two chunks apart by the ring's length).
+//
+// What bounds it is the chain gather -> S -> softmax -> O -> free of a part
+// (the MMAs take 16 x 48 + 8 x 128 = 1.8 K cycles of it), so the ring holds
+// four parts, each with its own S and P buffer, and two groups of four softmax
+// warps take alternate parts: while one waits on TMEM, shared memory or the
+// other's M, the other computes.  (128-entry parts, whose S runs at the full
+// MMA rate, with both groups on one part: 7 K cycles per 128 entries.)
 //
 // TMEM (512 columns): O in columns 0-255 (channels 0-255 in the lower 16
-// lanes of every lane quarter, 256-511 in the upper 16); two S buffers of 128
+// lanes of every lane quarter, 256-511 in the upper 16); four S buffers of 64
 // columns.  Lane quarter `sub` holds heads 16 sub .. + 15: their hi rows in
 // its lower 16 lanes, their lo rows in the upper 16.
 //
-// Warps (20): 0-7 gather codes (16-byte cp.async, one entry per warp and
-// instruction) and convert q; 8 fetches the entries' scale bytes; 9 issues S,
-// 10 issues O (one thread each), 11 owns TMEM; 12-19 softmax and epilogue.
-// The two softmax warps of a lane quarter take 64 entries of a tile each and
-// exchange their tile maxima through shared memory (xch).
-// Every wait is bounded (sm100::mbar_wait); the pairs meet on an mbarrier,
+// Warps (20): 0-3 gather codes (16-byte cp.async, one entry per warp and
+// instruction); 4-7 split q, a lane quarter each; 8 fetches the entries'
+// scales; 9 issues S, 10 issues O (one thread each); 11 owns TMEM and posts
+// the work items ahead of their consumers; 12-19 softmax and epilogue.
+// Every wait is bounded (sm100::mbar_wait); the groups meet on mbarriers,
 // never on a named barrier, so a wait that ran out cannot strand a partner.
 #pragma once
 #include "mqa_f8_simt.cuh"
@@ -59,36 +64,37 @@ struct MqaF8TcArgs {
   float scale_log2;                         // log2(e) / sqrt(c)
   RowMap rm;
   int splits;                               // work items per (row, head group)
-  int tiles_per_split;
+  int parts_per_split;
   float* part_o;                            // splits > 1: [rows, nh, splits, 512]
   float* part_lse;                          //             [rows, nh, splits], base 2; -inf: nothing seen
 };
 
 namespace mqaf8 {
-constexpr int kC = 512, kHeads = 64, kTile = 128, kPart = 64, kParts = 4;
+constexpr int kC = 512, kHeads = 64, kPart = 64, kParts = 4;
 constexpr int kChunk = kParts * kPart * 128;      // ring bytes of one 128-channel chunk
 constexpr int kQChunk = 128 * 128;                // q: 128 rows x 128 channels
-constexpr int kPHalf = 64 * 128;                  // 64 heads x 128 entries
-constexpr int kPBytes = 2 * kPHalf;               // hi, lo
+constexpr int kPBytes = 64 * 128;                 // P of a part: 64 heads x (64 hi | 64 lo)
 constexpr int kOffC = 4 * kQChunk;
-constexpr int kOffP = kOffC + 4 * kChunk;         // two P buffers; the epilogue's staging rows between items
-constexpr int kOffE = kOffP + 2 * kPBytes;        // scale byte of each ring entry
-constexpr int kOffX = kOffE + kParts * kPart;     // xch: [2][8 warps][16 heads] fp32
-constexpr int kOffS = kOffX + 2 * 8 * 16 * 4;     // q scale of each head
+constexpr int kOffP = kOffC + 4 * kChunk;         // kParts P buffers; the epilogue's staging rows between items
+constexpr int kOffE = kOffP + kParts * kPBytes;   // scale (fp32) of each ring entry
+constexpr int kOffX = kOffE + kParts * kPart * 4; // xch: [2 groups][64 heads] fp32
+constexpr int kOffS = kOffX + 2 * kHeads * 4;     // q scale of each head
 constexpr int kOffMisc = kOffS + kHeads * 4;
-constexpr size_t kSmem = 1024 + kOffMisc + 512;
+constexpr size_t kSmem = kOffMisc + 768;          // the swizzled tiles need a base aligned to 1024 bytes
 static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr int kItems = 4;                         // item descriptors in flight
+constexpr int kReaders = 4 + 4 + 3 + 8;           // warps that read each of them
 constexpr int kThreads = 640;
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
-// w <= 2^(kOff + kGrow) = 256 < 448: the running maximum may lag by kGrow
-constexpr float kOff = 6.f, kGrow = 2.f;
-constexpr float kLo = 32.f;                       // q: lo = 32 (q - hi) is at most 256
+// w <= 2^(kOff + kGrow) = 362 < 448: the running maximum may lag by kGrow, and
+// the largest weight stays above 2^kOff.  A rescale of O costs a part's time
+// (it waits for the products in flight), so kGrow is most of E4M3's range.
+constexpr float kOff = 3.5f, kGrow = 5.f;
 }  // namespace mqaf8
 
-// Tiles of 128 slots up to the row's last valid slot (0 <= s < avail), by a
-// whole warp; every warp role derives it from the index row.  The row is read
-// from its end, 512 slots at a time, so a full row costs one memory latency.
-__device__ __forceinline__ int mqa_f8_ntiles(const int* ir, int topk, int avail) {
+// Parts of 64 slots up to the row's last valid slot (0 <= s < avail), by a
+// whole warp.  The row is read from its end, 512 slots at a time, so a full row costs one memory latency.
+__device__ __forceinline__ int mqa_f8_nparts(const int* ir, int topk, int avail) {
   const int lane = threadIdx.x & 31;
   for (int j0 = ((topk - 1) / 512) * 512; j0 >= 0; j0 -= 512) {
     int v[16], last = -1;
@@ -101,26 +107,43 @@ __device__ __forceinline__ int mqa_f8_ntiles(const int* ir, int topk, int avail)
     for (int u = 0; u < 16; ++u)
       if (v[u] >= 0 && v[u] < avail) last = j0 + 32 * u + lane;
     last = __reduce_max_sync(0xffffffffu, last);
-    if (last >= 0) return last / mqaf8::kTile + 1;
+    if (last >= 0) return last / mqaf8::kPart + 1;
   }
   return 0;
 }
 
-// E4M3 pairs <-> fp16 pairs (hardware conversions).
-__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
-  uint16_t v;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(v) : "r"(h));
-  return v;
+// Four fp16 values (two pairs) as hi + lo, one byte each: hi their E4M3
+// rounding, lo the rest in E4M3 (or E5M2).  The rest is exact in fp16, so lo
+// also holds what hi lost to E4M3's range.
+#define CSA_SPLIT4(LO_TYPE)                                       \
+  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 p, q;\n\t"             \
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"                  \
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, %3;\n\t"                  \
+      "mov.b32 %0, {a, b};\n\t"                                   \
+      "cvt.rn.f16x2.e4m3x2 p, a;\n\t"                             \
+      "cvt.rn.f16x2.e4m3x2 q, b;\n\t"                             \
+      "sub.f16x2 p, %2, p;\n\t"                                   \
+      "sub.f16x2 q, %3, q;\n\t"                                   \
+      "cvt.rn.satfinite." LO_TYPE ".f16x2 a, p;\n\t"              \
+      "cvt.rn.satfinite." LO_TYPE ".f16x2 b, q;\n\t"              \
+      "mov.b32 %1, {a, b};\n\t}"                                  \
+      : "=r"(hi), "=r"(lo)                                        \
+      : "r"(h0), "r"(h1))
+__device__ __forceinline__ void split4_e4m3(uint32_t h0, uint32_t h1, uint32_t& hi, uint32_t& lo) {
+  CSA_SPLIT4("e4m3x2");
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  return h;
+__device__ __forceinline__ void split4_e4m3_e5m2(uint32_t h0, uint32_t h1, uint32_t& hi, uint32_t& lo) {
+  CSA_SPLIT4("e5m2x2");
+}
+#undef CSA_SPLIT4
+// Two fp32 values rounded to an fp16 pair.
+__device__ __forceinline__ uint32_t to_half2(float2 x) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 consecutive TMEM columns from `t0` and 32 from `t1`, 16 at a time, to
-// s[k] = a * x0[k] + b * x1[k] of the lane pair (L, L ^ 16): the lower lane
-// keeps columns t0 .., the upper one t1 .., each giving the other's away.
+// 16 consecutive fp32 TMEM columns of this thread's lane from `t0` and 16 from
+// `t1`, with a single wait.
 __device__ __forceinline__ void tmem_ld_x16_pair(uint32_t t0, uint32_t t1, float* v0, float* v1) {
   uint32_t r[32];
   asm volatile(
@@ -142,26 +165,71 @@ __device__ __forceinline__ void tmem_ld_x16_pair(uint32_t t0, uint32_t t1, float
   }
 }
 
+// Packed fp32 pairs (one instruction for two values).
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 upk2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float lg2_approx_f32(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A work item: its row, head group and split, and the parts [p0, p1) of the
+// row that it covers (none where p0 >= p1).
+struct MqaF8Item {
+  int row, hg, split, p0, p1, avail;
+  long long base;
+};
+
 __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcArgs a) {
   using namespace sm100;
   using namespace mqaf8;
   constexpr uint32_t kFull = 0xffffffffu;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* e_s = sm + kOffE;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (smem_u32(sm) & 1023u) {   // the declared alignment; the tiles' swizzle relies on it
+    flag_status(kStatusBounds);
+    return;
+  }
+  float* e_s = reinterpret_cast<float*>(sm + kOffE);
   float* xch = reinterpret_cast<float*>(sm + kOffX);
   float* qs_s = reinterpret_cast<float*>(sm + kOffS);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + kOffMisc);
   uint64_t* q_empty = q_full + 1;         // the item's last S done, and every softmax warp has its q scales
   uint64_t* c_full = q_empty + 1;         // [kParts] codes landed
-  uint64_t* e_full = c_full + kParts;     // [kParts] scale bytes and validity written
-  uint64_t* t_done = e_full + kParts;     // [kParts] O product of the part done (frees it)
-  uint64_t* s_full = t_done + kParts;     // [2]
-  uint64_t* s_free = s_full + 2;          // [2]
-  uint64_t* p_full = s_free + 2;          // [2]
-  uint64_t* o_free = p_full + 2;
-  uint64_t* x_bar = o_free + 1;           // [4] softmax pairs
-  uint32_t* valid_s = reinterpret_cast<uint32_t*>(x_bar + 4);   // [kParts][2] validity of the ring entries
+  uint64_t* e_full = c_full + kParts;     // [kParts] scales and validity written
+  uint64_t* t_done = e_full + kParts;     // [kParts] O product of the part done: frees its ring entries and P buffer
+  uint64_t* s_full = t_done + kParts;     // [kParts]
+  uint64_t* s_free = s_full + kParts;     // [kParts]
+  uint64_t* p_full = s_free + kParts;     // [kParts]
+  uint64_t* o_free = p_full + kParts;
+  uint64_t* x_bar = o_free + 1;           // [2 groups][4 lane quarters] a value posted in xch
+  uint64_t* it_full = x_bar + 8;          // [kItems] item descriptor posted
+  uint64_t* it_free = it_full + kItems;   // [kItems] read by its kReaders consumer warps
+  MqaF8Item* item_s = reinterpret_cast<MqaF8Item*>(it_free + kItems);
+  uint32_t* valid_s = reinterpret_cast<uint32_t*>(item_s + kItems);   // [kParts][2] validity of the ring entries
   uint32_t* tmem_slot = valid_s + 2 * kParts;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -171,20 +239,22 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
   const int items = a.rows * per_row;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 8);
+    mbar_init(q_full, 4);
     mbar_init(q_empty, 1 + 8);
     for (int s = 0; s < kParts; ++s) {
-      mbar_init(&c_full[s], 256);
+      mbar_init(&c_full[s], 128);
       mbar_init(&e_full[s], 1);
       mbar_init(&t_done[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], 8);
-      mbar_init(&p_full[s], 8);
+      mbar_init(&s_free[s], 4);
+      mbar_init(&p_full[s], 4);
     }
     mbar_init(o_free, 8);
-    for (int s = 0; s < 4; ++s) mbar_init(&x_bar[s], 2);
+    for (int s = 0; s < 8; ++s) mbar_init(&x_bar[s], 1);
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(&it_full[s], 1);
+      mbar_init(&it_free[s], kReaders);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -195,138 +265,142 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
   pdl_prologue_done();
   const uint32_t tmem = *tmem_slot;
 
-  // An item: its row and head group, and the tiles [t0, t1) of the row that
-  // it covers.  Rows run last first: they see the most entries.
-  struct Item {
-    int row, hg, split, t0, t1, avail;
-    long long base;
-    const int* ir;
-  };
-  auto item_of = [&](int it) {
-    Item w;
-    w.row = a.rows - 1 - it / per_row;
-    const int r = it % per_row;
-    w.hg = r / a.splits;
-    w.split = r - w.hg * a.splits;
-    row_entries(a.rm, w.row, w.base, w.avail);
-    w.ir = a.idx + (long long)w.row * a.topk;
-    const int n = mqa_f8_ntiles(w.ir, a.topk, w.avail);
-    w.t0 = w.split * a.tiles_per_split;
-    w.t1 = min(n, w.t0 + a.tiles_per_split);
-    return w;
+  // The n-th item of this CTA, as warp 11 posted it (a whole warp; false: a wait ran out).
+  auto item_of = [&](uint32_t n, MqaF8Item& w) {
+    const int slot = (int)(n % kItems);
+    const bool ok = warp_wait_small(&it_full[slot], (n / kItems) & 1);
+    w = item_s[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&it_free[slot]);
+    if (!ok && lane == 0) *abort_flag = 1;
+    return ok;
   };
 
-  if (warp < 8) {
-    // ------------------------------------------------------------ gather and q conversion (warps 0-7)
-    uint32_t g = 0, qw = 0;   // ring parts, items
+  if (warp < 4) {
+    // ------------------------------------------------------------ gather (warps 0-3)
+    // entry warp + 4 i of a part per instruction, a lane 16 bytes; slots fetched one part ahead
+    uint32_t g = 0, n = 0;   // ring parts, items
     bool ok = true;
+    const uint32_t ring = smem_u32(sm + kOffC + (lane >> 3) * kChunk);
+    const uint32_t swz0 = sw128(warp, lane & 7), swz1 = sw128(warp + 4, lane & 7);
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
-      const Item w = item_of(it);
-      if (w.t0 >= w.t1) continue;
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
+      if (w.p0 >= w.p1) continue;
       const long long n_ent = rowmap_entries(a.rm, a.rows);
-      // q: this warp's heads 8 warp .. + 7, a lane 16 channels of each (four heads in flight)
-      const __nv_bfloat16* qrow =
-          a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads + 8 * warp) * kC + 16 * lane;
-#pragma unroll 1
-      for (int hb = 0; hb < 2; ++hb) {
-        uint4 raw[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) raw[i][u] = __ldg(reinterpret_cast<const uint4*>(qrow + (4 * hb + i) * kC) + u);
-        if (hb == 0 && !warp_wait(q_empty, (qw & 1) ^ 1)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t* rw = reinterpret_cast<const uint32_t*>(raw[i]);
-          uint32_t m = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t x0 = (rw[e] << 16) & 0x7FFFFFFFu, x1 = rw[e] & 0x7FFF0000u;
-            m = max(m, max(x0 < 0x7F800000u ? x0 : 0u, x1 < 0x7F800000u ? x1 : 0u));
-          }
-          m = __reduce_max_sync(kFull, m);
-          // 2^-k with the largest value in [128, 256)
-          const uint32_t ex = max(m >> 23, 8u);
-          const float inv = __uint_as_float((261u - ex) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            hi[q] = 0;
-            lo[q] = 0;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint32_t wd = rw[2 * q + p];
-              float x0 = __uint_as_float(wd << 16), x1 = __uint_as_float(wd & 0xFFFF0000u);
-              x0 = fabsf(x0) < INFINITY ? x0 * inv : NAN;
-              x1 = fabsf(x1) < INFINITY ? x1 * inv : NAN;
-              const uint32_t h = f8::f32x2_to_e4m3(x0, x1);
-              const float2 hf = f8::e4m3x2_to_f32((uint16_t)h);
-              hi[q] |= h << (16 * p);
-              lo[q] |= f8::f32x2_to_e4m3((x0 - hf.x) * kLo, (x1 - hf.y) * kLo) << (16 * p);
-            }
-          }
-          const int head = 8 * warp + 4 * hb + i;
-          const int r = 32 * (head >> 4) + (head & 15);
-          uint8_t* dst = sm + (lane >> 3) * kQChunk;
-          *reinterpret_cast<uint4*>(dst + sw128(r, lane & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + sw128(r + 16, lane & 7)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (lane == 0) qs_s[head] = __uint_as_float((ex - 7u) << 23);
-        }
-      }
-      if (!ok) break;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      ++qw;
-      // codes: entry warp + 8 i of a part per instruction, a lane 16 bytes; slots fetched one part ahead
-      const int p0 = 2 * w.t0, p1 = 2 * w.t1;
+      const int* ir = a.idx + (long long)w.row * a.topk;
       auto slot = [&](int p) {
-        const int e = p * kPart + warp + 8 * lane;
-        return lane < 8 && e < a.topk ? __ldg(w.ir + e) : -1;
+        const int e = p * kPart + warp + 4 * lane;
+        return lane < 16 && e < a.topk ? __ldg(ir + e) : -1;
       };
-      int next = slot(p0);
-      for (int p = p0; p < p1; ++p, ++g) {
+      const uint8_t* src0 = a.codes + w.base * kC + 16 * lane;
+      int next = slot(w.p0);
+      for (int p = w.p0; p < w.p1; ++p, ++g) {
         const int st = (int)(g % kParts);
         const int mine = next;
-        next = p + 1 < p1 ? slot(p + 1) : -1;
-        if (!warp_wait(&t_done[st], ((g / kParts) & 1) ^ 1)) { ok = false; break; }
-        uint8_t* dst = sm + kOffC + (lane >> 3) * kChunk + st * kPart * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        next = p + 1 < w.p1 ? slot(p + 1) : -1;
+        if (!warp_wait_small(&t_done[st], ((g / kParts) & 1) ^ 1)) { ok = false; break; }
+        // rows warp + 4 i: two swizzle phases, 1024 bytes every other row
+        const uint32_t dst = ring + (uint32_t)(st * kPart * 128);
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
           const int s = __shfl_sync(kFull, mine, i);
-          const bool v = s >= 0 && s < w.avail && dcheck(w.base + s < n_ent);
-          const uint8_t* src = v ? a.codes + (w.base + s) * kC + 16 * lane : a.codes;
-          cp_async16(dst + sw128(warp + 8 * i, lane & 7), src, v ? 16u : 0u);
+          const bool v = (unsigned)s < (unsigned)w.avail && dcheck(w.base + s < n_ent);
+          cp_async16_to(dst + ((i & 1) ? swz1 : swz0) + (uint32_t)(i >> 1) * 1024u, v ? src0 + (long long)s * kC : a.codes,
+                        v ? 16u : 0u);
         }
         cp_async_arrive_noinc(&c_full[st]);
       }
     }
     if (!ok && lane == 0) *abort_flag = 1;
     cp_async_wait_all();
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ scale bytes and validity
-    uint32_t g = 0;
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ q split (warps 4-7)
+    // heads 16 (warp - 4) .. + 15, a lane 16 channels of each
+    const int sub = warp - 4;
+    uint32_t qw = 0, n = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
-      const Item w = item_of(it);
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
+      if (w.p0 >= w.p1) continue;
+      const __nv_bfloat16* qrow =
+          a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads + 16 * sub) * kC + 16 * lane;
       bool ok = true;
-      for (int p = 2 * w.t0; p < 2 * w.t1; ++p, ++g) {
+      uint4 raw[4][2];   // 16 values of four heads, on their way
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) raw[i][u] = __ldg(reinterpret_cast<const uint4*>(qrow + i * kC) + u);
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int b = i & 3;
+        const uint32_t rw[8] = {raw[b][0].x, raw[b][0].y, raw[b][0].z, raw[b][0].w,
+                                raw[b][1].x, raw[b][1].y, raw[b][1].z, raw[b][1].w};
+        if (i < 12)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) raw[b][u] = __ldg(reinterpret_cast<const uint4*>(qrow + (i + 4) * kC) + u);
+        uint32_t m2 = 0;   // the larger magnitude of each half
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, rw[e] & 0x7FFF7FFFu);
+        const uint32_t m = __reduce_max_sync(kFull, max(m2 & 0xFFFFu, m2 >> 16));
+        // 2^-k with the largest value in [128, 256).  An infinite or NaN
+        // value gives a NaN lo, and with it NaN scores.
+        const uint32_t ex = max(m >> 7, 8u);
+        const float inv = __uint_as_float((261u - ex) << 23);
+        const uint64_t inv2 = pk2(inv, inv);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[2];   // exact in fp16: 8 bits, below 256
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t wd = rw[2 * q + p];
+            h[p] = to_half2(upk2(mul2(pk2(__uint_as_float(wd << 16), __uint_as_float(wd & 0xFFFF0000u)), inv2)));
+          }
+          split4_e4m3(h[0], h[1], hi[q], lo[q]);
+        }
+        if (i == 0 && !warp_wait_small(q_empty, (qw & 1) ^ 1)) { ok = false; break; }
+        uint8_t* dst = sm + (lane >> 3) * kQChunk;
+        *reinterpret_cast<uint4*>(dst + sw128(32 * sub + i, lane & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + sw128(32 * sub + 16 + i, lane & 7)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (lane == 0) qs_s[16 * sub + i] = __uint_as_float((ex - 7u) << 23);
+      }
+      if (!ok) {
+        if (lane == 0) *abort_flag = 1;
+        break;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      ++qw;
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ scales and validity
+    uint32_t g = 0, n = 0;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+      if (warp_aborted(abort_flag)) break;
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
+      const int* ir = a.idx + (long long)w.row * a.topk;
+      bool ok = true;
+      for (int p = w.p0; p < w.p1; ++p, ++g) {
         const int st = (int)(g % kParts);
         bool v[2];
         uint32_t b[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int e = p * kPart + 32 * u + lane;
-          const int s = e < a.topk ? __ldg(w.ir + e) : -1;
+          const int s = e < a.topk ? __ldg(ir + e) : -1;
           v[u] = s >= 0 && s < w.avail;
           if (!v[u] && s != -1) flag_status(kStatusBadIndex);
           b[u] = v[u] ? __ldg(a.scales + w.base + s) : 0u;
         }
-        if (!warp_wait(&t_done[st], ((g / kParts) & 1) ^ 1)) { ok = false; break; }
+        if (!warp_wait_small(&t_done[st], ((g / kParts) & 1) ^ 1)) { ok = false; break; }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          e_s[st * kPart + 32 * u + lane] = (uint8_t)b[u];
+          e_s[st * kPart + 32 * u + lane] = f8::scale_value(b[u]);
           const uint32_t m = __ballot_sync(kFull, v[u]);
           if (lane == 0) valid_s[2 * st + u] = m;
         }
@@ -339,299 +413,344 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
       }
     }
   } else if (warp == 9) {
-    // ------------------------------------------------------------ S issuer (lane 0)
-    constexpr uint32_t idS = idesc_e4m3_f32(128, kTile);
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t idS = idesc_e4m3_f32(128, kPart);
     const uint64_t qd0 = sdesc_k_sw128(smem_u32(sm));
     const uint64_t cd0 = sdesc_k_sw128(smem_u32(sm + kOffC));
-    uint32_t g = 0, qw = 0;   // tiles, items
+    uint32_t g = 0, qw = 0, n = 0;   // parts, items with parts, items
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
-      const Item w = item_of(it);
-      if (w.t0 >= w.t1) continue;
-      int ok = 1;
-      if (lane == 0) {
-        if (!mbar_wait(q_full, qw & 1)) ok = 0;
-        for (int j = w.t0; ok && j < w.t1; ++j) {
-          const uint32_t gj = g + (uint32_t)(j - w.t0);
-          const int sb = (int)(gj & 1), st = (int)((2 * gj) % kParts);
-          const uint32_t ph = (2 * gj / kParts) & 1;
-          if (!mbar_wait(&c_full[st], ph) || !mbar_wait(&c_full[st + 1], ph) ||
-              !mbar_wait(&s_free[sb], ((gj >> 1) & 1) ^ 1)) {
-            ok = 0;
-            break;
-          }
-          fence_proxy_async_smem();
-          tc_fence_after();
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
+      const int np = w.p1 - w.p0;
+      if (np <= 0) continue;
+      bool ok = warp_wait_small(q_full, qw & 1);
+      for (int j = 0; ok && j < np; ++j, ++g) {
+        const int st = (int)(g % kParts);
+        const uint32_t ph = (g / kParts) & 1;
+        if (!warp_wait_small(&c_full[st], ph) || !warp_wait_small(&s_free[st], ph ^ 1)) { ok = false; break; }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t cd = desc_add(cd0, st * kPart * 128);
 #pragma unroll
           for (int kc = 0; kc < 4; ++kc)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_f8(tmem + kColS + 128u * (uint32_t)sb, desc_add(qd0, kc * kQChunk + ks * 32),
-                     desc_add(cd0, kc * kChunk + st * kPart * 128 + ks * 32), idS, (kc | ks) != 0 ? 1u : 0u);
-          mma_commit(&s_full[sb]);
-          if (j == w.t1 - 1) mma_commit(q_empty);
+              mma_f8(tmem + kColS + (uint32_t)(kPart * st), desc_add(qd0, kc * kQChunk + ks * 32),
+                     desc_add(cd, kc * kChunk + ks * 32), idS, (kc | ks) != 0 ? 1u : 0u);
+          mma_commit(&s_full[st]);
+          if (j == np - 1) mma_commit(q_empty);
         }
+        __syncwarp();
       }
-      ok = __shfl_sync(kFull, ok, 0);
       if (!ok) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
       ++qw;
-      g += (uint32_t)(w.t1 - w.t0);
     }
   } else if (warp == 10) {
-    // ------------------------------------------------------------ O issuer (lane 0)
-    constexpr uint32_t idO = idesc_e4m3_f32(64, 256) | (1u << 16);   // B is MN-major
+    // ------------------------------------------------------------ O issuer
+    constexpr uint32_t idHi = idesc_e4m3_f32(64, 256) | (1u << 16);   // B is MN-major
+    constexpr uint32_t idLo = idHi | (1u << 7);                       // A is E5M2
     const uint64_t vd0 = sdesc_mn_sw128(smem_u32(sm + kOffC), kChunk, 1024);
     const uint64_t pd0 = sdesc_k_sw128(smem_u32(sm + kOffP));
-    uint32_t g = 0, oi = 0;
+    uint32_t g = 0, oi = 0, n = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
-      const Item w = item_of(it);
-      if (w.t0 >= w.t1) continue;
-      int ok = 1;
-      if (lane == 0) {
-        for (int j = w.t0; j < w.t1; ++j) {
-          const uint32_t gj = g + (uint32_t)(j - w.t0);
-          const int pb = (int)(gj & 1), st = (int)((2 * gj) % kParts);
-          if (!mbar_wait(&p_full[pb], (gj >> 1) & 1) ||
-              (j == w.t0 && !mbar_wait(o_free, (oi & 1) ^ 1))) {   // the previous item's O has been read
-            ok = 0;
-            break;
-          }
-          tc_fence_after();
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
+      const int np = w.p1 - w.p0;
+      if (np <= 0) continue;
+      bool ok = warp_wait_small(o_free, (oi & 1) ^ 1);   // the previous item's O has been read
+      for (int j = 0; ok && j < np; ++j, ++g) {
+        const int st = (int)(g % kParts);
+        if (!warp_wait_small(&p_full[st], (g / kParts) & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t pd = desc_add(pd0, st * kPBytes), vd = desc_add(vd0, st * kPart * 128);
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
+            for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
-              for (int hl = 0; hl < 2; ++hl)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                  mma_f8(tmem + ((uint32_t)(16 * hh) << 16) + kColO,
-                         desc_add(pd0, pb * kPBytes + hl * kPHalf + (2 * p + ks) * 32),
-                         desc_add(vd0, 2 * hh * kChunk + ((st + p) * kPart + 32 * ks) * 128), idO,
-                         (j > w.t0 || p > 0 || ks > 0 || hl > 0) ? 1u : 0u);
-            mma_commit(&t_done[st + p]);
-          }
+              for (int hh = 0; hh < 2; ++hh)
+                mma_f8(tmem + ((uint32_t)(16 * hh) << 16) + kColO, desc_add(pd, 64 * hl + 32 * ks),
+                       desc_add(vd, 2 * hh * kChunk + 32 * ks * 128), hl ? idLo : idHi,
+                       (j > 0 || ks > 0 || hl > 0) ? 1u : 0u);
+          mma_commit(&t_done[st]);
         }
+        __syncwarp();
       }
-      ok = __shfl_sync(kFull, ok, 0);
       if (!ok) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
       ++oi;
-      g += (uint32_t)(w.t1 - w.t0);
     }
-  } else if (warp >= 12) {
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ item scheduler
+    // Rows run last first: they see the most entries.  A lane looks up the
+    // row of one of 32 items; each item's index row is then scanned for its
+    // parts, up to kItems items ahead of their consumers.
+    uint32_t n = 0;
+    bool ok = true;
+    for (unsigned it0 = blockIdx.x; it0 < (unsigned)items && ok; it0 += 32u * gridDim.x) {
+      const unsigned mine = it0 + (unsigned)lane * gridDim.x;   // items + 32 CTAs per SM stay below 2^32
+      int row = 0, avail = 0, hg = 0, split = 0;
+      long long base = 0;
+      if (mine < (unsigned)items) {
+        const unsigned q = mine / (unsigned)per_row, r = mine - q * (unsigned)per_row;
+        row = a.rows - 1 - (int)q;
+        hg = (int)(r / (unsigned)a.splits);
+        split = (int)(r - (unsigned)hg * (unsigned)a.splits);
+        row_entries(a.rm, row, base, avail);
+      }
+#pragma unroll 1
+      for (unsigned u = 0; u < 32 && it0 + u * gridDim.x < (unsigned)items; ++u, ++n) {
+        if (warp_aborted(abort_flag)) { ok = false; break; }
+        MqaF8Item w;
+        w.row = __shfl_sync(kFull, row, u);
+        w.avail = __shfl_sync(kFull, avail, u);
+        w.base = __shfl_sync(kFull, base, u);
+        w.hg = __shfl_sync(kFull, hg, u);
+        w.split = __shfl_sync(kFull, split, u);
+        const int parts = mqa_f8_nparts(a.idx + (long long)w.row * a.topk, a.topk, w.avail);
+        w.p0 = w.split * a.parts_per_split;
+        w.p1 = min(parts, w.p0 + a.parts_per_split);
+        if (w.p0 < w.p1) {   // 64 heads x 1 KB of q on their way to L2 (from memory at prefill)
+          const __nv_bfloat16* q = a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads) * kC + 64 * lane;
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) prefetch_l2(q + i * 4 * kC);
+        }
+        const int slot = (int)(n % kItems);
+        if (!warp_wait_small(&it_free[slot], ((n / kItems) & 1) ^ 1)) {
+          if (lane == 0) *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          item_s[slot] = w;
+          mbar_arrive(&it_full[slot]);
+        }
+      }
+    }
+  } else {
     // ------------------------------------------------------------ softmax and epilogue (warps 12-19)
-    const int sub = warp & 3, ch = (warp - 12) >> 2;   // lane quarter; half of the tile / of the O columns
-    const int half = lane >> 4;                        // which 32 of the warp's 64 entries
-    const int hrow = 16 * sub + (lane & 15);           // head of the group
+    const int sub = warp & 3, grp = (warp - 12) >> 2;   // lane quarter; parts of this parity / half of the O columns
+    const int half = lane >> 4;                         // which 32 of a part's entries
+    const int hrow = 16 * sub + (lane & 15);            // head of the group
     const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
-    float* x_mine = xch + (4 * ch + sub) * 16 + (lane & 15);
-    float* x_other = xch + (4 * (ch ^ 1) + sub) * 16 + (lane & 15);
-    uint32_t g = 0, qw = 0, xn = 0;   // tiles, items, exchanges
-    // value of the partner warp's same head; both warps take part
-    auto exchange = [&](float v, float& other) {
-      float* slot = x_mine + 128 * (xn & 1);
-      if (half == 0) *slot = v;
+    uint32_t g = 0, qw = 0, n = 0;      // parts, items with parts, items
+    uint32_t seen_n = 0;                // values of the other group's warp read so far
+    // Values go from a group's warp to the other group's warp of the same
+    // lane quarter and come back in turn, so one slot each is enough.
+    auto post = [&](float v) {
+      if (half == 0) xch[grp * kHeads + hrow] = v;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&x_bar[sub]);
-      const bool ok = warp_wait(&x_bar[sub], xn & 1);
-      other = x_other[128 * (xn & 1)];
-      ++xn;
+      if (lane == 0) mbar_arrive(&x_bar[4 * grp + sub]);
+    };
+    auto receive = [&](float& v) {
+      const bool ok = warp_wait_small(&x_bar[4 * (grp ^ 1) + sub], seen_n & 1);
+      ++seen_n;
+      v = xch[(grp ^ 1) * kHeads + hrow];
       return ok;
     };
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
-      const Item w = item_of(it);
+      MqaF8Item w;
+      if (!item_of(n++, w)) break;
       const int head = w.hg * kHeads + hrow;
-      if (w.t0 >= w.t1) {   // nothing to see
+      if (w.p0 >= w.p1) {   // nothing to see
         if (a.splits > 1) {
-          if (ch == 0 && half == 0) a.part_lse[((long long)w.row * a.nh + head) * a.splits + w.split] = -INFINITY;
+          if (grp == 0 && half == 0) a.part_lse[((long long)w.row * a.nh + head) * a.splits + w.split] = -INFINITY;
         } else {
           uint4* o = reinterpret_cast<uint4*>(a.O + (long long)w.row * a.ld_O + (long long)head * kC + 256 * half +
-                                              128 * ch);
+                                              128 * grp);
           for (int i = 0; i < 16; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
         continue;
       }
-      bool ok = warp_wait(q_full, qw & 1);
+      bool ok = warp_wait_small(q_full, qw & 1);
       const float qs = ok ? qs_s[hrow] * a.scale_log2 : 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty);
       ++qw;
-      // S = ca * own + cb * partner's: the lower lanes own hi and get lo, the upper ones the reverse
-      const float ca = half ? qs / kLo : qs, cb = half ? qs : qs / kLo;
+      const uint64_t qs2 = pk2(qs, qs);
       float R = -INFINITY, l = 0.f;    // this lane's running maximum of s, and its sum of 2^(s - R)
-      float M = -INFINITY;             // the head's (lagging) maximum of s + e
-      const int tiles = w.t1 - w.t0;
-      for (int j = 0; ok && j < tiles; ++j) {
+      float M = -INFINITY;             // the head's (lagging) maximum of s + log2(scale)
+      const int np = w.p1 - w.p0;
+      const uint32_t glast = g + (uint32_t)np - 1;
+      for (int j = (int)((g ^ (uint32_t)grp) & 1); ok && j < np; j += 2) {
         const uint32_t gj = g + (uint32_t)j;
-        const int sb = (int)(gj & 1), st = (int)((2 * gj) % kParts) + ch;
-        const uint32_t ph = (2 * gj / kParts) & 1;
-        if (!warp_wait(&e_full[st], ph) || !warp_wait(&s_full[sb], (gj >> 1) & 1)) { ok = false; break; }
+        const int st = (int)(gj % kParts);
+        const uint32_t ph = (gj / kParts) & 1;
+        if (!warp_wait_small(&e_full[st], ph) || !warp_wait_small(&s_full[st], ph)) { ok = false; break; }
         tc_fence_after();
-        float s[32];
-        const uint32_t col = tmem + lane_base + kColS + 128u * (uint32_t)sb + 64u * (uint32_t)ch;
+        uint64_t v[16];   // s of this lane's 32 entries, in pairs
+        const uint32_t col = tmem + lane_base + kColS + (uint32_t)(kPart * st);
+        const ulonglong2* ep = reinterpret_cast<const ulonglong2*>(e_s + st * kPart + 32 * half);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           float x0[16], x1[16];
           tmem_ld_x16_pair(col + 16u * b, col + 32u + 16u * b, x0, x1);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float other = __shfl_xor_sync(kFull, half ? x0[k] : x1[k], 16);
-            s[16 * b + k] = fmaf(cb, other, ca * (half ? x1[k] : x0[k]));
+          for (int k = 0; k < 16; k += 2) {
+            const float o0 = __shfl_xor_sync(kFull, half ? x0[k] : x1[k], 16);
+            const float o1 = __shfl_xor_sync(kFull, half ? x0[k + 1] : x1[k + 1], 16);
+            v[8 * b + k / 2] =   // hi + lo: one's own column plus the partner lane's
+                mul2(qs2, add2(pk2(o0, o1), half ? pk2(x1[k], x1[k + 1]) : pk2(x0[k], x0[k + 1])));
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[sb]);
-        // entry scales: s to its value, and the maxima of s and of s + e
-        uint32_t eb[8];
-        {
-          const uint4* ep = reinterpret_cast<const uint4*>(e_s + st * kPart + 32 * half);
-          const uint4 e0 = ep[0], e1 = ep[1];
-          eb[0] = e0.x; eb[1] = e0.y; eb[2] = e0.z; eb[3] = e0.w;
-          eb[4] = e1.x; eb[5] = e1.y; eb[6] = e1.z; eb[7] = e1.w;
+        if (lane == 0) mbar_arrive(&s_free[st]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const ulonglong2 e = ep[k];
+          v[2 * k] = mul2(v[2 * k], e.x);
+          v[2 * k + 1] = mul2(v[2 * k + 1], e.y);
         }
         const uint32_t vm = valid_s[2 * st + half];
-        float smax = -INFINITY, tmax = -INFINITY;
+        if (vm != kFull) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t byte = (eb[k >> 2] >> (8 * (k & 3))) & 0xFFu;
-          s[k] *= __uint_as_float(byte << 23);   // byte 0 (2^-127) reads as zero
-          if (!((vm >> k) & 1u)) s[k] = -INFINITY;
-          smax = fmaxf(smax, s[k]);
-          tmax = fmaxf(tmax, s[k] + (float)byte);
+          for (int k = 0; k < 16; ++k) {
+            float2 x = upk2(v[k]);
+            if (!((vm >> (2 * k)) & 1u)) x.x = -INFINITY;
+            if (!((vm >> (2 * k + 1)) & 1u)) x.y = -INFINITY;
+            v[k] = pk2(x.x, x.y);
+          }
         }
+        // probabilities relative to this lane's running maximum R, their sum, and
+        // u = p scale, whose maximum gives that of s + log2(scale)
+        float Rn = R;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = upk2(v[k]);
+          Rn = max3(Rn, x.x, x.y);
+        }
+        const float Ru = Rn == -INFINITY ? 0.f : Rn;
+        l *= ex2_approx_f32(R - Ru);
+        R = Rn;
+        float umax = 0.f;
+        {
+          const uint64_t mr2 = pk2(-Ru, -Ru);
+          uint64_t l2 = pk2(l, 0.f);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const ulonglong2 e = ep[k / 2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float2 x = upk2(add2(v[k + q], mr2));
+              const uint64_t p = pk2(ex2_approx_f32(x.x), ex2_approx_f32(x.y));
+              l2 = add2(l2, p);
+              v[k + q] = mul2(p, q ? e.y : e.x);
+              const float2 u = upk2(v[k + q]);
+              umax = max3(umax, u.x, u.y);
+            }
+          }
+          const float2 ls = upk2(l2);
+          l = ls.x + ls.y;
+        }
+        float tmax = Ru + lg2_approx_f32(umax);   // log2(0) = -inf
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 16));
-        float other;
-        if (!exchange(tmax, other)) { ok = false; break; }
-        tmax = fmaxf(tmax, other) - 127.f;
-        const bool grow = tmax > M + kGrow;   // also on the first tile with a valid entry
+        if (j > 0 && !receive(M)) { ok = false; break; }   // M after the part before
+        const bool grow = tmax > M + kGrow;   // also on the first part with a valid entry
         const float Mn = grow ? tmax : M;
-        // P buffer (and, to rescale O, every earlier O product) free?
-        if (__any_sync(kFull, grow && j > 0)) {
-          const uint32_t gp = 2 * (gj - 1) + 1;
-          if (!warp_wait(&t_done[gp % kParts], (gp / kParts) & 1)) { ok = false; break; }
+        post(Mn);
+        if (__any_sync(kFull, grow && j > 0)) {   // rescale O: its earlier products must have completed
+          const uint32_t gp = gj - 1;
+          if (!warp_wait_small(&t_done[gp % kParts], (gp / kParts) & 1)) { ok = false; break; }
           tc_fence_after();
           const float alpha = grow ? ex2_approx_f32(M - Mn) : 1.f;   // 2^-inf = 0 when nothing was seen
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            const uint32_t ta = tmem + lane_base + kColO + 128u * (uint32_t)ch + 32u * (uint32_t)c;
-            tmem_ld_32x32b_x32(ta, v);
+          for (int c = 0; c < 8; ++c) {
+            float o[32];
+            const uint32_t ta = tmem + lane_base + kColO + 32u * (uint32_t)c;
+            tmem_ld_32x32b_x32(ta, o);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] *= alpha;
-            tmem_st_32x32b_x32(ta, v);
+            for (int q = 0; q < 32; ++q) o[q] *= alpha;
+            tmem_st_32x32b_x32(ta, o);
           }
           tmem_st_wait();
           tc_fence_before();
         }
         M = Mn;
-        const float Rn = fmaxf(R, smax), Ru = Rn == -INFINITY ? 0.f : Rn;
-        l *= ex2_approx_f32(R - Ru);
-        R = Rn;
-        // w = 2^(s - R) 2^e 2^(R - M + kOff)
+        // w = u 2^(R - M + kOff), as hi + lo.  The part's P buffer is free: its S could only be issued on ring
+        // entries that the O product of four parts before, the buffer's last reader, had released.
         const float f = ex2_approx_f32(fminf(Ru - (M == -INFINITY ? 0.f : M) + kOff, 126.f));
+        const uint64_t f2 = pk2(f, f);
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          hi[q] = 0;
-          lo[q] = 0;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int k = 4 * q + 2 * p;
-            const float p0 = ex2_approx_f32(s[k] - Ru), p1 = ex2_approx_f32(s[k + 1] - Ru);
-            l += p0 + p1;
-            const uint32_t b0 = (eb[q] >> (16 * p)) & 0xFFu, b1 = (eb[q] >> (16 * p + 8)) & 0xFFu;
-            const __half2 w2 = __floats2half2_rn(p0 * __uint_as_float(b0 << 23) * f, p1 * __uint_as_float(b1 << 23) * f);
-            const uint16_t h8 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&w2));
-            const uint32_t hb = e4m3x2_to_half2(h8);
-            const __half2 rest = __hsub2(w2, *reinterpret_cast<const __half2*>(&hb));
-            hi[q] |= (uint32_t)h8 << (16 * p);
-            lo[q] |= (uint32_t)f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest)) << (16 * p);
-          }
-        }
-        const int pb = (int)(gj & 1);
-        if (gj >= 2) {   // the P buffer's previous reader
-          const uint32_t gp = 2 * (gj - 2) + 1;
-          if (!warp_wait(&t_done[gp % kParts], (gp / kParts) & 1)) { ok = false; break; }
-        }
-        uint8_t* prow = sm + kOffP + pb * kPBytes;
-        const int u = 4 * ch + 2 * half;
-        *reinterpret_cast<uint4*>(prow + sw128(hrow, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(prow + sw128(hrow, u + 1)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        *reinterpret_cast<uint4*>(prow + kPHalf + sw128(hrow, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(prow + kPHalf + sw128(hrow, u + 1)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        for (int q = 0; q < 8; ++q)
+          split4_e4m3_e5m2(to_half2(upk2(mul2(v[2 * q], f2))), to_half2(upk2(mul2(v[2 * q + 1], f2))), hi[q], lo[q]);
+        uint8_t* prow = sm + kOffP + st * kPBytes;
+        *reinterpret_cast<uint4*>(prow + sw128(hrow, 2 * half)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(prow + sw128(hrow, 2 * half + 1)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+        *reinterpret_cast<uint4*>(prow + sw128(hrow, 4 + 2 * half)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(prow + sw128(hrow, 5 + 2 * half)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[pb]);
+        if (lane == 0) mbar_arrive(&p_full[st]);
       }
-      // the head's normaliser relative to M: this lane's, its pair's, the partner warp's
-      const bool seen = M != -INFINITY;
-      float lm = seen && l > 0.f ? l * ex2_approx_f32(fminf(R - M, 126.f)) : l;
+      // the head's M is that of the item's last part; its normaliser, relative to M, is the sum of both groups'
+      const bool last_mine = (int)(glast & 1) == grp;
+      if (ok && !last_mine) ok = receive(M);
+      float lm = l > 0.f && M != -INFINITY ? l * ex2_approx_f32(fminf(R - M, 126.f)) : l;
       lm += __shfl_xor_sync(kFull, lm, 16);
-      float lo_other = 0.f;
-      if (ok && !exchange(lm, lo_other)) ok = false;
-      const uint32_t glast = 2 * (g + (uint32_t)tiles - 1) + 1;
-      if (!ok || !warp_wait(&t_done[glast % kParts], (glast / kParts) & 1)) {
+      float lother = 0.f;
+      if (ok && !last_mine) post(lm);
+      if (ok) ok = receive(lother);
+      if (ok && last_mine) post(lm);
+      if (!ok || !warp_wait_small(&t_done[glast % kParts], (glast / kParts) & 1)) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const float lsum = lm + lo_other;
+      const float lsum = grp == 0 ? lm + lother : lother + lm;   // the same sum in both groups
       const float inv = lsum == 0.f ? 0.f : exp2f(-kOff) / lsum;
-      // O / l in two passes of 64 columns per lane.  bf16 rows go through 32 staging rows (row = lane: head
-      // 16 sub + lane % 16, channels 256 (lane / 16) + 128 ch + 64 p ..) that alias this quarter's rows of P
-      // buffer `ch`: its next writers are the two warps of this quarter, after both have met again.
-      uint8_t* stage = sm + kOffP + ch * kPBytes + 16 * sub * 128;
-      auto stage_row = [&](int r) { return stage + (r >> 4) * kPHalf; };
+      // O / l in four passes of 32 columns per lane.  bf16 rows go through 32 staging rows of 64 bytes (row = lane:
+      // head 16 sub + lane % 16, channels 256 (lane / 16) + 128 grp + 32 p ..) that alias this quarter's rows of P
+      // buffer grp, which only this warp writes.
+      uint8_t* stage = sm + kOffP + grp * kPBytes + 16 * sub * 128;
+      __nv_bfloat16* ob = a.O + (long long)w.row * a.ld_O + (long long)(w.hg * kHeads + 16 * sub) * kC + 128 * grp;
+      float* po = a.part_o + (((long long)w.row * a.nh + head) * a.splits + w.split) * kC + 256 * half + 128 * grp;
 #pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
-        float v0[32], v1[32];
-        const uint32_t ta = tmem + lane_base + kColO + 128u * (uint32_t)ch + 64u * (uint32_t)p;
-        tmem_ld_32x32b_x32_pair(ta, ta + 32u, v0, v1);
-        if (p == 1) {   // O is in registers: the next item's O products may start
+      for (int p = 0; p < 4; ++p) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128u * (uint32_t)grp + 32u * (uint32_t)p, v);
+        if (p == 3) {   // O is in registers: the next item's O products may start
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free);
         }
         if (a.splits > 1) {
-          float4* o = reinterpret_cast<float4*>(
-              a.part_o + (((long long)w.row * a.nh + head) * a.splits + w.split) * kC + 256 * half + 128 * ch + 64 * p);
+          float4* o = reinterpret_cast<float4*>(po + 32 * p);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            o[q] = make_float4(v0[4 * q] * inv, v0[4 * q + 1] * inv, v0[4 * q + 2] * inv, v0[4 * q + 3] * inv);
-            o[8 + q] = make_float4(v1[4 * q] * inv, v1[4 * q + 1] * inv, v1[4 * q + 2] * inv, v1[4 * q + 3] * inv);
-          }
+          for (int q = 0; q < 8; ++q)
+            o[q] = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
           continue;
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* vv = u < 4 ? v0 : v1;
+        for (int u = 0; u < 4; ++u) {
           Vec16<__nv_bfloat16> pk;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) pk.e[q] = __float2bfloat16_rn(vv[8 * (u & 3) + q] * inv);
-          *reinterpret_cast<uint4*>(stage_row(lane) + sw128(lane & 15, u)) = pk.u;
+          for (int q = 0; q < 8; ++q) pk.e[q] = __float2bfloat16_rn(v[8 * u + q] * inv);
+          *reinterpret_cast<uint4*>(stage + sw64(lane, u)) = pk.u;
         }
         __syncwarp();
-        __nv_bfloat16* ob = a.O + (long long)w.row * a.ld_O + (long long)(w.hg * kHeads + 16 * sub) * kC;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), u = lane & 7;
-          const uint4 val = *reinterpret_cast<const uint4*>(stage_row(r) + sw128(r & 15, u));
-          *reinterpret_cast<uint4*>(ob + (r & 15) * kC + 256 * (r >> 4) + 128 * ch + 64 * p + 8 * u) = val;
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), u = lane & 3;
+          const uint4 val = *reinterpret_cast<const uint4*>(stage + sw64(r, u));
+          *reinterpret_cast<uint4*>(ob + (r & 15) * kC + 256 * (r >> 4) + 32 * p + 8 * u) = val;
         }
         __syncwarp();
       }
-      if (a.splits > 1 && ch == 0 && half == 0)
+      if (a.splits > 1 && grp == 0 && half == 0)
         a.part_lse[((long long)w.row * a.nh + head) * a.splits + w.split] = lsum == 0.f ? -INFINITY : M + log2f(lsum);
-      g += (uint32_t)tiles;
+      g += (uint32_t)np;
     }
   }
   tc_fence_before();

@@ -82,6 +82,43 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same waits with the polling loop out of line: a call site is one
+// try_wait (which itself sleeps until the phase completes, or for the hint)
+// and a call that is reached only after it ran out.  For kernels whose many
+// roles would otherwise not fit the instruction cache.
+__device__ __noinline__ bool mbar_wait_again(uint32_t addr, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_wait_ns);
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    if (done) return true;
+    if (global_ns() - t0 > limit || i >= kMaxPolls) {
+      flag_status(kStatusTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  if (!__all_sync(0xffffffffu, done)) done = mbar_wait_again(addr, parity);
+  return __all_sync(0xffffffffu, done);
+}
+
 // Warp-uniform read of a CTA abort flag (lane 0's view).
 __device__ __forceinline__ bool warp_aborted(volatile int* flag) {
   return __shfl_sync(0xffffffffu, *flag, 0) != 0;
@@ -343,6 +380,9 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_add
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16_to(uint32_t dst_smem, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(src_bytes) : "memory");
 }
 // Arrive on `bar` (without raising its pending count) once every cp.async
 // this thread issued so far has landed; the barrier's expected count must

@@ -103,9 +103,12 @@ def gemm(a, b, dtype):
 def mqa(q, codes, scales, sel, dtype):
     """One query row: q [nh, c] float64, entries codes [*, c] / scales [*], sel = the valid entry rows.
     -> output [nh, c] and its bound for a kernel with
-      s: an exact product up to 2^-22 of q's row maximum per channel, sums in fp32 (one step 2^-23 per addition),
-      softmax weight times scale: within 2^-8 + 2^-10 relative (two E4M3 parts, the fp16 value they are taken from,
-        the exponential), and 2^-16 of the head's largest one (the parts' smallest step),
+      q: hi + lo, both E4M3, of the row scaled to a maximum in [128, 256): 8 significant bits are kept unless lo is
+        subnormal (half of its step: 2^-10, that is 2^-17 of the row's maximum);
+      scores: sums in fp32, one step 2^-23 per addition;
+      weight times scale w = hi + lo, hi E4M3, lo E5M2, of a value rounded to fp16 (2^-11): hi is within 2^-4 of w
+        (2^-10 where it is subnormal), lo within 2^-3 of the rest, so w is within 2^-7 + 2^-11 relative and 2^-13, or
+        2^-17 where lo is subnormal: at most 2^-13 in all, of a largest weight of 2^3.5 or more: 2^-16.5 of it;
       and one rounding to dtype."""
     nh, c = q.shape
     if sel.numel() == 0:
@@ -119,8 +122,8 @@ def mqa(q, codes, scales, sel, dtype):
     p = torch.softmax(s, 1)
     o = p @ e
     ds = ((c + 4) * 2.0 ** -23 * (q.abs() @ e.abs().t())
-          + 2.0 ** -22 * q.abs().amax(1, keepdim=True) * e.abs().sum(1)[None]) / math.sqrt(c) + 2.0 ** -20 * (1 + s.abs())
+          + 2.0 ** -17 * q.abs().amax(1, keepdim=True) * e.abs().sum(1)[None]) / math.sqrt(c) + 2.0 ** -20 * (1 + s.abs())
     dp = p * torch.expm1(2 * ds)                     # numerator and normaliser both move by exp(ds)
     floor = 2.0 ** -16 * (p * sc).amax(1, keepdim=True)
-    bound = ((2.0 ** -8 + 2.0 ** -10) * p + dp) @ e.abs() + dp.sum(1, keepdim=True) * o.abs() + floor * raw.abs().sum(0)[None]
+    bound = ((2.0 ** -7 + 2.0 ** -10) * p + dp) @ e.abs() + dp.sum(1, keepdim=True) * o.abs() + floor * raw.abs().sum(0)[None]
     return o, bound + half_step(dtype) * (o.abs() + bound) + 1e-37
