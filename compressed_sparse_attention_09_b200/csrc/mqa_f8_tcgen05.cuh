@@ -204,6 +204,78 @@ struct MqaF8Item {
   long long base;
 };
 
+// Splits the query rows of heads `h0` .. h0 + heads - 1 of an item's 64 into
+// the swizzled q tile, by a whole warp (a lane 16 channels of each head): two
+// heads at a time, so that one's reduction and conversions fill the other's
+// latencies, with the next two on their way.  heads is a multiple of 4.
+// `empty`: the tile's release, waited for before the first store.  Out of line:
+// both the q warps and, for a CTA's first item, the softmax warps run it.
+__device__ __noinline__ bool mqa_f8_split_q(const __nv_bfloat16* q64, int h0, int heads, uint8_t* sm, float* qs_s,
+                                            uint64_t* empty, uint32_t parity) {
+  using namespace mqaf8;
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* qrow = q64 + (long long)h0 * kC + 16 * lane;
+  uint4 raw[2][2][2];   // [pair of heads in flight][head][16 bytes]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) raw[i >> 1][i & 1][u] = __ldg(reinterpret_cast<const uint4*>(qrow + i * kC) + u);
+  uint8_t* dst = sm + (lane >> 3) * kQChunk;
+#pragma unroll 1
+  for (int i0 = 0; i0 < heads; i0 += 4) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int i = i0 + 2 * b;
+      uint32_t rw[2][8], ex[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 r0 = raw[b][k][0], r1 = raw[b][k][1];
+        rw[k][0] = r0.x; rw[k][1] = r0.y; rw[k][2] = r0.z; rw[k][3] = r0.w;
+        rw[k][4] = r1.x; rw[k][5] = r1.y; rw[k][6] = r1.z; rw[k][7] = r1.w;
+        if (i + 4 < heads)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) raw[b][k][u] = __ldg(reinterpret_cast<const uint4*>(qrow + (i + 4 + k) * kC) + u);
+        __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);   // the larger magnitude of each half
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&rw[k][e])));
+        const uint32_t m = *reinterpret_cast<const uint32_t*>(&m2);
+        ex[k] = max(m & 0xFFFFu, m >> 16);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) ex[k] = max(__reduce_max_sync(0xffffffffu, ex[k]) >> 7, 8u);
+      uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // 2^-k with the largest value in [128, 256).  An infinite or NaN
+        // value gives a NaN lo, and with it NaN scores.
+        const float inv = __uint_as_float((261u - ex[k]) << 23);
+        const uint64_t inv2 = pk2(inv, inv);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[2];   // exact in fp16: 8 bits, below 256
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t wd = rw[k][2 * q + p];
+            h[p] = to_half2(upk2(mul2(pk2(__uint_as_float(wd << 16), __uint_as_float(wd & 0xFFFF0000u)), inv2)));
+          }
+          split4_e4m3(h[0], h[1], hi[k][q], lo[k][q]);
+        }
+      }
+      if (i == 0 && !sm100::warp_wait_small(empty, parity)) return false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int head = h0 + i + k, r = 32 * (head >> 4) + (head & 15);
+        *reinterpret_cast<uint4*>(dst + sw128(r, lane & 7)) = make_uint4(hi[k][0], hi[k][1], hi[k][2], hi[k][3]);
+        *reinterpret_cast<uint4*>(dst + sw128(r + 16, lane & 7)) = make_uint4(lo[k][0], lo[k][1], lo[k][2], lo[k][3]);
+        if (lane == 0) qs_s[head] = __uint_as_float((ex[k] - 7u) << 23);
+      }
+    }
+  }
+  sm100::fence_proxy_async_smem();
+  __syncwarp();
+  return true;
+}
+
 __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcArgs a) {
   using namespace sm100;
   using namespace mqaf8;
@@ -239,7 +311,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
   const int items = a.rows * per_row;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 16);
     mbar_init(q_empty, 1 + 8);
     for (int s = 0; s < kParts; ++s) {
       mbar_init(&c_full[s], 128);
@@ -317,63 +389,23 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
     cp_async_wait_all();
   } else if (warp < 8) {
     // ------------------------------------------------------------ q split (warps 4-7)
-    // heads 16 (warp - 4) .. + 15, a lane 16 channels of each
-    const int sub = warp - 4;
+    // 16 heads each; of the first item 4 each, the softmax warps taking the
+    // other 48 (they have nothing else to do yet)
     uint32_t qw = 0, n = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
       MqaF8Item w;
       if (!item_of(n++, w)) break;
       if (w.p0 >= w.p1) continue;
-      const __nv_bfloat16* qrow =
-          a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads + 16 * sub) * kC + 16 * lane;
-      bool ok = true;
-      uint4 raw[4][2];   // 16 values of four heads, on their way
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) raw[i][u] = __ldg(reinterpret_cast<const uint4*>(qrow + i * kC) + u);
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int b = i & 3;
-        const uint32_t rw[8] = {raw[b][0].x, raw[b][0].y, raw[b][0].z, raw[b][0].w,
-                                raw[b][1].x, raw[b][1].y, raw[b][1].z, raw[b][1].w};
-        if (i < 12)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) raw[b][u] = __ldg(reinterpret_cast<const uint4*>(qrow + (i + 4) * kC) + u);
-        uint32_t m2 = 0;   // the larger magnitude of each half
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, rw[e] & 0x7FFF7FFFu);
-        const uint32_t m = __reduce_max_sync(kFull, max(m2 & 0xFFFFu, m2 >> 16));
-        // 2^-k with the largest value in [128, 256).  An infinite or NaN
-        // value gives a NaN lo, and with it NaN scores.
-        const uint32_t ex = max(m >> 7, 8u);
-        const float inv = __uint_as_float((261u - ex) << 23);
-        const uint64_t inv2 = pk2(inv, inv);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t h[2];   // exact in fp16: 8 bits, below 256
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint32_t wd = rw[2 * q + p];
-            h[p] = to_half2(upk2(mul2(pk2(__uint_as_float(wd << 16), __uint_as_float(wd & 0xFFFF0000u)), inv2)));
-          }
-          split4_e4m3(h[0], h[1], hi[q], lo[q]);
-        }
-        if (i == 0 && !warp_wait_small(q_empty, (qw & 1) ^ 1)) { ok = false; break; }
-        uint8_t* dst = sm + (lane >> 3) * kQChunk;
-        *reinterpret_cast<uint4*>(dst + sw128(32 * sub + i, lane & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + sw128(32 * sub + 16 + i, lane & 7)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (lane == 0) qs_s[16 * sub + i] = __uint_as_float((ex - 7u) << 23);
-      }
-      if (!ok) {
+      const __nv_bfloat16* q64 = a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads) * kC;
+      const bool first = qw == 0;
+      const int heads = first ? 4 : 16;
+      if (!mqa_f8_split_q(q64, (warp - 4) * heads, heads, sm, qs_s, q_empty, (qw & 1) ^ 1)) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0)
+        for (int u = 0; u < (first ? 1 : 4); ++u) mbar_arrive(q_full);
       ++qw;
     }
   } else if (warp == 8) {
@@ -572,7 +604,17 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         }
         continue;
       }
-      bool ok = warp_wait_small(q_full, qw & 1);
+      bool ok = true;
+      if (qw == 0) {   // a share of the first item's q
+        const __nv_bfloat16* q64 = a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads) * kC;
+        if (warp < 16) ok = mqa_f8_split_q(q64, 16 + 8 * (warp - 12), 8, sm, qs_s, q_empty, 1u);
+        else ok = mqa_f8_split_q(q64, 48 + 4 * (warp - 16), 4, sm, qs_s, q_empty, 1u);
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          if (warp < 16) mbar_arrive(q_full);
+        }
+      }
+      ok = ok && warp_wait_small(q_full, qw & 1);
       const float qs = ok ? qs_s[hrow] * a.scale_log2 : 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty);
