@@ -1503,7 +1503,7 @@ csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8
   const TcGemmArgs& g = a.g;
   const int tiles = ((g.M + Cfg::BM - 1) / Cfg::BM) * ((g.N + BN - 1) / BN) * g.k_split;
   const int grid = tiles < sm_count() ? tiles : sm_count();
-  if (launch_pdl(k, dim3(grid), dim3(224), Cfg::SMEM, st, ta, tb, a) != cudaSuccess) return CSA_ERR_CUDA;
+  if (launch_pdl(k, dim3(grid), dim3(kF8GemmThreads), Cfg::SMEM, st, ta, tb, a) != cudaSuccess) return CSA_ERR_CUDA;
   CSA_CHECK_LAUNCH();
   if (g.k_split > 1) {
     const int m_pad = ((g.M + Cfg::BM - 1) / Cfg::BM) * Cfg::BM;
@@ -1517,12 +1517,12 @@ csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8
 }
 
 // K slices of a product with few rows (weights as the 128-row operand): as
-// many as fill the SMs, each at least two K blocks.
+// many as fill the SMs, each a multiple of four K blocks (one group of scales).
 int f8_gemm_splits(int M, int N, int K) {
   if (M > 64) return 1;
   const int w_tiles = (N + 127) / 128, k_blocks = (K + 127) / 128;
   for (int ks = 8; ks >= 2; ks /= 2)
-    if ((long long)w_tiles * ks <= sm_count() && k_blocks % ks == 0 && k_blocks / ks >= 2) return ks;
+    if ((long long)w_tiles * ks <= sm_count() && k_blocks % (4 * ks) == 0) return ks;
   return 1;
 }
 size_t f8_gemm_ws(int M, int N, int K) {
@@ -1544,8 +1544,8 @@ csa_status launch_gemm_f8(const void* A, long long lda, const void* sa, long lon
   a.g.out = out;
   a.g.k_split = 1;
   a.g.part = nullptr;
-  const ScaleRows rows_a{static_cast<const uint8_t*>(sa), ld_sa, 1, M};
-  const ScaleRows rows_b{static_cast<const uint8_t*>(sb), ld_sb, f8::kBlock, N};
+  const ScaleRows rows_a{static_cast<const uint8_t*>(sa), ld_sa, 0, M};
+  const ScaleRows rows_b{static_cast<const uint8_t*>(sb), ld_sb, 7, N};
   if (M <= 64) {   // few rows: the weights fill the 128-row operand, the epilogue transposes
     if (!make_tmap_u8(&ta, B, K, N, (uint64_t)ldb, 128, 128) || !make_tmap_u8(&tb, A, K, M, (uint64_t)lda, 128, 64))
       return CSA_ERR_UNSUPPORTED;

@@ -16,14 +16,14 @@
 // four consecutive bytes of a scale row, go into one cell: one copy of scales
 // per 512 values of K.
 //
-// Persistent, warp-specialised CTA (one per SM, 224 threads):
+// Persistent, warp-specialised CTA (one per SM, 352 threads):
 //   warp 0      TMA producer: 128 x 128 codes of A and BN x 128 of B per
 //               stage, K-major with 128-byte swizzle;
 //   warp 1      owns TMEM; one thread copies scales to TMEM (tcgen05.cp),
 //               issues tcgen05.mma (M = 128, N = BN, K = 32) and commits;
-//   warps 2..5  epilogue (gemm_store_cols64 of gemm_tcgen05.cuh);
-//   warp 6      reads the scale bytes of four K blocks at a time into shared
-//               memory in the order tcgen05.cp takes, one group ahead.
+//   warp 2      reads the scale bytes of four K blocks at a time into shared
+//               memory in the order tcgen05.cp takes, one group ahead;
+//   warps 3..10 epilogue, two per TMEM lane quarter.
 // Two accumulators (2 x BN columns) let a tile's epilogue overlap the next
 // tile's products; the other columns hold kSfBufs sets of scales.  Scale
 // buffer b (shared memory and TMEM) is refilled only after the last product
@@ -35,10 +35,13 @@
 namespace csa {
 
 struct ScaleRows {
-  const uint8_t* p; long long ld;   // byte of row r, K block b: p[(r / div) * ld + b]
-  int div;                          // 1, or 128 for weights
+  const uint8_t* p; long long ld;   // byte of row r, K block b: p[(r >> shift) * ld + b]
+  int shift;                        // 0, or 7 for weights (one byte for 128 rows)
   int rows;                         // operand rows
 };
+
+constexpr int kF8EpiWarps = 8;                      // two per TMEM lane quarter, half of the columns each
+constexpr int kF8GemmThreads = 32 * (3 + kF8EpiWarps);
 
 struct F8GemmArgs {
   TcGemmArgs g;       // M: rows of the 128-row operand, N: of the other one
@@ -56,26 +59,112 @@ struct F8GemmCfg {
   static constexpr int kSfBufs = 4;
   static constexpr int TMEM_COLS = 2 * BN + kSfBufs * SF_COLS <= 256 ? 256 : 512;
   static_assert(2 * BN + kSfBufs * SF_COLS <= 512, "accumulators and scales share TMEM");
-  static constexpr int OUT_STAGE = 4 * 32 * 128;
+  static constexpr int OUT_STAGE = kF8EpiWarps * 32 * 64;   // staging: 32 rows of 64 B per epilogue warp
   static constexpr size_t SMEM =
       1024 /*align slack*/ + (size_t)kStages * STAGE_BYTES + OUT_STAGE + (size_t)kSfBufs * SF_BYTES + 256 /*barriers*/;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// The scale bytes of K blocks 4 q .. 4 q + 3 of operand row r (127, a scale
-// of one, where there is no such row or block: the codes there are zero).
-__device__ __forceinline__ uint32_t scale_word(const ScaleRows& s, int r, int q, int k_blocks) {
-  if (r >= s.rows) return 0x7F7F7F7Fu;
-  const uint8_t* p = s.p + (long long)(r / s.div) * s.ld + 4 * q;
-  if (4 * q + 4 <= k_blocks && (reinterpret_cast<uintptr_t>(p) & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(p));
+// The scale bytes of K blocks 4 q .. 4 q + 3 from a row's byte 4 q on, byte by
+// byte (a row's ragged end, or rows that are not 4-byte aligned); 127, a scale
+// of one, past the last block: the codes there are zero.
+__device__ __noinline__ uint32_t scale_bytes(const uint8_t* p, int left) {
   uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (uint32_t)(4 * q + i < k_blocks ? __ldg(p + i) : 127) << (8 * i);
+  for (int i = 0; i < 4; ++i) w |= (uint32_t)(i < left ? __ldg(p + i) : 127) << (8 * i);
   return w;
+}
+// The same as one word where that is possible.  p: NULL for a row past the matrix.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int q, int k_blocks, bool words) {
+  if (!p) return 0x7F7F7F7Fu;
+  if (words && 4 * q + 4 <= k_blocks) return __ldg(reinterpret_cast<const uint32_t*>(p) + q);
+  return scale_bytes(p + 4 * q, k_blocks - 4 * q);
+}
+__device__ __forceinline__ const uint8_t* scale_row(const ScaleRows& s, int r) {
+  return r < s.rows ? s.p + (long long)(r >> s.shift) * s.ld : nullptr;
+}
+
+// byte offset of 16-byte piece u (0..3) of row r in 64-byte rows, XOR-swizzled
+__device__ __forceinline__ uint32_t r_sw64(int r, int u) { return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)); }
+
+// ---------------------------------------------------------------- epilogue
+// The MMAs of a tile take half the time of a bf16 tile's, so the epilogue
+// must be short: the destination is worked out once per tile, and where the
+// tile's columns lie in one segment with 16-byte aligned rows, a step is 32
+// columns through the warp's staging rows (row = lane) and out as 64-byte
+// pieces of rows.  Anything else (a ragged
+// edge, an odd row stride, several segments) takes the general store.
+struct F8Dest {
+  uint8_t* p;      // row 0 of this warp's 32, column 0 of its range; NULL: general store
+  long long pitch; // bytes between rows
+  int rows;        // rows in range
+  int f32;
+};
+
+// Destination of rows r0 .. r0 + 31, columns c0 .. c0 + cols - 1.
+__device__ __forceinline__ F8Dest f8_dest(const TcGemmArgs& g, int r0, int c0, int cols) {
+  F8Dest d;
+  d.p = nullptr;
+  d.pitch = 0;
+  d.f32 = 0;
+  d.rows = min(32, g.M - r0);
+  if (g.transpose_out || g.k_split > 1 || c0 + cols > g.N) return d;
+#pragma unroll 1
+  for (int s = 0; s < g.out.nseg; ++s) {
+    const OutSeg& sg = g.out.seg[s];
+    if (c0 < sg.col0 || c0 + cols > sg.col0 + sg.ncols) continue;
+    const int es = sg.f32 ? 4 : 2;
+    const long long pitch = sg.ld * es;
+    uint8_t* p = static_cast<uint8_t*>(sg.ptr) + (long long)r0 * pitch + (long long)(c0 - sg.col0) * es;
+    if ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch) & 15) return d;
+    d.p = p;
+    d.pitch = pitch;
+    d.f32 = sg.f32;
+  }
+  return d;
+}
+
+// 64 bytes of each of this warp's rows (32 bf16 or 16 fp32 columns) through
+// the staging rows: eight rows per store instruction.
+__device__ __forceinline__ void f8_store_rows(const F8Dest& d, int byte0, const uint4* v, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(stage + r_sw64(lane, u)) = v[u];
+  __syncwarp();
+  const int r0 = lane >> 2, u = lane & 3;
+  uint8_t* p = d.p + (long long)r0 * d.pitch + byte0 + 16 * u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + r_sw64(r0 + 8 * i, u));
+    if (r0 + 8 * i < d.rows) *reinterpret_cast<uint4*>(p) = x;
+    p += 8 * d.pitch;
+  }
+  __syncwarp();
+}
+
+// The general store, out of line: it is long and rarely runs.
+__device__ __noinline__ void f8_store_general(const TcGemmArgs& g, int m_tiles, int mt, int sub, int ks, int c0, int acc_addr,
+                                              uint8_t* stage) {
+  float v0[32], v1[32];
+  sm100::tmem_ld_32x32b_x32(acc_addr, v0);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v1[j] = 0.f;
+  TcGemmArgs h = g;
+  h.N = min(g.N, c0 + 32);   // these 32 columns only
+  if (g.k_split > 1) {       // (the slice layout goes by the whole N)
+    const int r = mt * kGemmRows + sub * 32 + (threadIdx.x & 31);
+    const size_t ld = (size_t)m_tiles * kGemmRows;
+    float* dst = g.part + (size_t)ks * g.N * ld + r;
+    if (r < g.M)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j < g.N) dst[(size_t)(c0 + j) * ld] = v0[j];
+    return;
+  }
+  gemm_store_cols64(h, m_tiles, mt, sub, ks, c0, v0, v1, stage);
 }
 
 template <int BN, int kStages>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(kF8GemmThreads, 1)
     gemm_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, F8GemmArgs a) {
   using Cfg = F8GemmCfg<BN, kStages>;
   using namespace sm100;
@@ -99,7 +188,7 @@ __global__ void __launch_bounds__(224, 1)
   const int m_tiles = (g.M + Cfg::BM - 1) / Cfg::BM;
   const int n_tiles = (g.N + BN - 1) / BN;
   const int k_blocks = (g.K + Cfg::BK - 1) / Cfg::BK;
-  const int kbs = (k_blocks + g.k_split - 1) / g.k_split;   // K blocks per work unit
+  const int kbs = (k_blocks + g.k_split - 1) / g.k_split;   // K blocks per work unit (split: a multiple of 4)
   const int total = m_tiles * n_tiles * g.k_split;          // work units: (tile, K slice)
 
   if (threadIdx.x == 0) {
@@ -109,7 +198,7 @@ __global__ void __launch_bounds__(224, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], 4);
+      mbar_init(&tempty[s], kF8EpiWarps);
     }
     for (int s = 0; s < Cfg::kSfBufs; ++s) {
       mbar_init(&sf_full[s], 1);
@@ -146,68 +235,97 @@ __global__ void __launch_bounds__(224, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---------------- MMA issuer
+      // One thread's instructions set the pace (an MMA takes BN / 2 cycles), so
+      // a group of four K blocks is unrolled: the scale bytes' place in their
+      // cells is a constant, descriptors and barriers advance by one add.
       constexpr uint32_t idesc = idesc_mxe4m3(Cfg::BM, BN, 0);
+      const uint64_t ad0 = sdesc_k_sw128(smem_u32(smA)), bd0 = sdesc_k_sw128(smem_u32(smB));
+      const uint32_t full0 = smem_u32(full), sf_full0 = smem_u32(sf_full), sf_smem0 = smem_u32(smSf);
       int stage = 0, acc = 0, sb = 0;
       uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
-      for (int unit = blockIdx.x; unit < total && !*abort_flag; unit += gridDim.x) {
+      bool ok = true;
+      for (int unit = blockIdx.x; unit < total && ok && !*abort_flag; unit += gridDim.x) {
         const int kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1)) { *abort_flag = 1; break; }
+        if (!mbar_wait_small(smem_u32(&tempty[acc]), acc_phase ^ 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; ok && kb < kb1; kb += 4) {
           const uint32_t sf_tmem = tmem_base + (uint32_t)(2 * BN + sb * Cfg::SF_COLS);
-          if (kb == kb0 || (kb & 3) == 0) {   // a new group of four K blocks: its scales to TMEM
-            if (!mbar_wait(&sf_full[sb], sf_phase)) { *abort_flag = 1; break; }
-            tc_fence_after();
-            const uint32_t sf_smem = smem_u32(smSf + sb * Cfg::SF_BYTES);
-#pragma unroll
-            for (int i = 0; i < 1 + Cfg::SFB_GROUPS; ++i)
-              tmem_cp_scales(sf_tmem + 4u * (uint32_t)i, sf_smem + 512u * (uint32_t)i);
-          }
-          if (!mbar_wait(&full[stage], phase)) { *abort_flag = 1; break; }
+          if (!mbar_wait_small(sf_full0 + 8u * (uint32_t)sb, sf_phase)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t ad = sdesc_k_sw128(smem_u32(smA + stage * Cfg::A_BYTES));
-          const uint64_t bd = sdesc_k_sw128(smem_u32(smB + stage * Cfg::B_BYTES));
-          const uint32_t sf_id = (uint32_t)(kb & 3);
 #pragma unroll
-          for (int k = 0; k < Cfg::BK / 32; ++k)
-            mma_mxf8(d_tmem, desc_add(ad, k * 32), desc_add(bd, k * 32), idesc | (sf_id << 4) | (sf_id << 29),
-                     (kb != kb0 || k != 0) ? 1u : 0u, sf_tmem, sf_tmem + 4u);
-          mma_commit(&empty[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
-          if ((kb & 3) == 3 || kb == kb1 - 1) {
-            mma_commit(&sf_empty[sb]);
-            if (++sb == Cfg::kSfBufs) { sb = 0; sf_phase ^= 1; }
+          for (int i = 0; i < 1 + Cfg::SFB_GROUPS; ++i)
+            tmem_cp_scales(sf_tmem + 4u * (uint32_t)i, sf_smem0 + (uint32_t)(sb * Cfg::SF_BYTES + 512 * i));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kb + i < kb1) {
+              if (!mbar_wait_small(full0 + 8u * (uint32_t)stage, phase)) { ok = false; break; }
+              tc_fence_after();
+              const uint64_t ad = desc_add(ad0, stage * Cfg::A_BYTES), bd = desc_add(bd0, stage * Cfg::B_BYTES);
+#pragma unroll
+              for (int k = 0; k < Cfg::BK / 32; ++k)
+                mma_mxf8(d_tmem, desc_add(ad, k * 32), desc_add(bd, k * 32),
+                         idesc | ((uint32_t)i << 4) | ((uint32_t)i << 29), (kb != kb0 || i != 0 || k != 0) ? 1u : 0u,
+                         sf_tmem, sf_tmem + 4u);
+              mma_commit(&empty[stage]);
+              if (++stage == kStages) { stage = 0; phase ^= 1; }
+            }
           }
+          mma_commit(&sf_empty[sb]);
+          if (++sb == Cfg::kSfBufs) { sb = 0; sf_phase ^= 1; }
         }
         mma_commit(&tfull[acc]);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
+      if (!ok) *abort_flag = 1;
     }
-  } else if (warp < 6) {  // ---------------- epilogue warps 2..5
-    const int sub = warp & 3;   // TMEM lane quarter this warp may access
-    uint8_t* stage_out = smOut + (warp - 2) * (32 * 128);
+  } else if (warp >= 3) {  // ---------------- epilogue warps 3..10
+    const int sub = warp & 3;                  // TMEM lane quarter this warp may access
+    const int e = warp - 3;
+    constexpr int kCols = BN / 2;              // this warp's columns
+    const int col0 = (e >> 2) * kCols;
+    uint8_t* stage_out = smOut + e * (32 * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int unit = blockIdx.x; unit < total && !*abort_flag; unit += gridDim.x) {
       const int tile = unit / g.k_split, ks = unit % g.k_split;
       int mt, nt;
       gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
+      const int c0 = nt * BN + col0;
+      const F8Dest d = f8_dest(g, mt * Cfg::BM + 32 * sub, c0, kCols);
       if (!mbar_wait(&tfull[acc], acc_phase)) { *abort_flag = 1; break; }
       tc_fence_after();
+      __syncwarp();
+      const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * BN + col0);
 #pragma unroll 1
-      for (int ch = 0; ch < BN / 64; ++ch) {
-        float v0[32], v1[32];
-        const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * BN + ch * 64);
-        tmem_ld_32x32b_x32_pair(ta, ta + 32u, v0, v1);
-        gemm_store_cols64(g, m_tiles, mt, sub, ks, nt * BN + ch * 64, v0, v1, stage_out);
+      for (int c = 0; c < kCols; c += 32) {
+        if (!d.p) {
+          if (c0 + c < g.N) f8_store_general(g, m_tiles, mt, sub, ks, c0 + c, (int)(ta + c), stage_out);
+          continue;
+        }
+        float v[32];
+        tmem_ld_32x32b_x32(ta + (uint32_t)c, v);
+        if (d.f32) {
+          f8_store_rows(d, 4 * c, reinterpret_cast<const uint4*>(v), stage_out);
+          f8_store_rows(d, 4 * c + 64, reinterpret_cast<const uint4*>(v + 16), stage_out);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          f8_store_rows(d, 2 * c, reinterpret_cast<const uint4*>(w), stage_out);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
-  } else {  // ---------------- scale loader (warp 6)
+  } else {  // ---------------- scale loader (warp 2)
+    const bool words_a = ((reinterpret_cast<uintptr_t>(a.sa.p) | (uintptr_t)a.sa.ld) & 3) == 0;
+    const bool words_b = ((reinterpret_cast<uintptr_t>(a.sb.p) | (uintptr_t)a.sb.ld) & 3) == 0;
     int sb = 0;
     uint32_t sf_phase = 0;
     for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
@@ -215,15 +333,20 @@ __global__ void __launch_bounds__(224, 1)
       const int tile = unit / g.k_split, kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
       int mt, nt;
       gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
+      const uint8_t *ra[4], *rb[4 * Cfg::SFB_GROUPS];   // scale rows of this lane's operand rows
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ra[j] = scale_row(a.sa, mt * Cfg::BM + 32 * j + lane);
+#pragma unroll
+      for (int j = 0; j < 4 * Cfg::SFB_GROUPS; ++j)
+        rb[j] = 32 * j < BN ? scale_row(a.sb, nt * BN + 32 * j + lane) : nullptr;
       bool ok = true;
-      for (int q = kb0 >> 2; q <= (kb1 - 1) >> 2; ++q) {
+      for (int q = kb0 >> 2; 4 * q < kb1; ++q) {
         uint32_t wa[4], wb[4 * Cfg::SFB_GROUPS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wa[j] = scale_word(a.sa, mt * Cfg::BM + 32 * j + lane, q, k_blocks);
+        for (int j = 0; j < 4; ++j) wa[j] = scale_word(ra[j], q, k_blocks, words_a);
 #pragma unroll
-        for (int j = 0; j < 4 * Cfg::SFB_GROUPS; ++j)
-          wb[j] = 32 * j < BN ? scale_word(a.sb, nt * BN + 32 * j + lane, q, k_blocks) : 0x7F7F7F7Fu;
-        if (!warp_wait(&sf_empty[sb], sf_phase ^ 1)) { ok = false; break; }
+        for (int j = 0; j < 4 * Cfg::SFB_GROUPS; ++j) wb[j] = scale_word(rb[j], q, k_blocks, words_b);
+        if (!warp_wait_small(&sf_empty[sb], sf_phase ^ 1)) { ok = false; break; }
         uint4* dst = reinterpret_cast<uint4*>(smSf + sb * Cfg::SF_BYTES) + lane;
         dst[0] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
 #pragma unroll

@@ -105,7 +105,18 @@ __device__ __noinline__ bool mbar_wait_again(uint32_t addr, uint32_t parity) {
     }
   }
 }
-__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_small(uint32_t addr, uint32_t parity) {   // one thread
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  return done ? true : mbar_wait_again(addr, parity);
+}
+__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity) {   // a converged warp
   const uint32_t addr = smem_u32(bar);
   uint32_t done;
   asm volatile(
