@@ -150,10 +150,21 @@ def _p(x):
     return x.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            if raw and dev:   # the handle itself, without a Stream object (3 us of every call)
+                torch.cuda.current_stream()   # initialises CUDA
+                _current_stream = lambda: raw(dev())   # noqa: E731
+            else:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -292,23 +292,30 @@ __device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_
   }
   if constexpr (C8) {
     if (threadIdx.x >= 32 && threadIdx.x < 64) {   // beside the key entry's warp
-      const int lane = threadIdx.x & 31, units = c / f8::kUnit;   // c <= 1024: at most two units per lane
-      f8::Unit<T> x[2];
+      // bf16 entries of up to 1024 channels: at most four vectors of eight per lane
+      const int lane = threadIdx.x & 31;
+      f8::Vec<__nv_bfloat16> x[4];
       uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (lane + 32 * k < units) x[k].load_shared(c_s + (lane + 32 * k) * f8::kUnit);
-        else x[k].clear();
+      for (int k = 0; k < 4; ++k) {
+        x[k].v = make_uint4(0, 0, 0, 0);
+        if (8 * (lane + 32 * k) < c) x[k].v = *reinterpret_cast<const uint4*>(c_s + 8 * (lane + 32 * k));
         top = max(top, x[k].amax());
       }
       top = __reduce_max_sync(0xffffffffu, top);
+      const bool inf = top >= f8::kInfBits;
+      if (inf) {
+        top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, x[k].amax_finite());
+        top = __reduce_max_sync(0xffffffffu, top);
+      }
       const int sb = f8::scale_byte(top);
       const float inv = f8::inv_scale(sb);
       const long long e = (long long)b * a.cap + i;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (lane + 32 * k < units)
-          *reinterpret_cast<uint4*>(a.Ccodes + e * c + (lane + 32 * k) * f8::kUnit) = x[k].encode(inv);
+      for (int k = 0; k < 4; ++k)
+        if (8 * (lane + 32 * k) < c) x[k].encode_to(a.Ccodes + e * c + 8 * (lane + 32 * k), inv, inf);
       if (lane == 0) a.Cscale[e] = (uint8_t)sb;
     }
   }

@@ -71,6 +71,19 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Raises a kernel's dynamic shared memory limit, once per kernel and device
+// (the call costs about a microsecond of a launch).
+template <typename... KArgs>
+bool allow_smem(void (*kernel)(KArgs...), size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 // NVTX ranges around each stage's launches (host side), compiled in only
 // with -DCSA_NVTX so that a profiler timeline shows the stages by name.
 #ifdef CSA_NVTX
@@ -1452,6 +1465,13 @@ namespace {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Warp steps of a row (32 16-byte vectors each), and the CTAs of so many steps.
+long long f8_steps_per_row(int dtype, int w) {
+  const int step = 32 * (dtype == CSA_BF16 ? 8 : 4);
+  return (w + step - 1) / step;
+}
+unsigned f8_step_ctas(unsigned steps) { return (steps + 8 * f8::kSteps - 1) / (8 * f8::kSteps); }
+
 csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t st) {
   CSA_RANGE("quantize_f8");
   if (a.n == 0) return CSA_OK;
@@ -1464,14 +1484,14 @@ csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t s
     CSA_CHECK_LAUNCH();
     return CSA_OK;
   }
-  // threads are numbered in 32 bits: more than that many in several launches
-  const long long per = 8ll * ((a.w + f8::kBlock - 1) / f8::kBlock);
+  // warp steps are numbered in 32 bits: more than that many in several launches
+  const long long per = f8_steps_per_row(dtype, a.w);
   const int step = (int)std::max(1ll, std::min<long long>(a.n, (1ll << 30) / per));
   for (int r = 0; r < a.n; r += step) {
     a.row0 = r;
-    const unsigned units = (unsigned)(per * std::min(step, a.n - r)), grid = (units + 255) / 256;
-    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, dim3(grid), dim3(256), 0, st, a, units)
-                            : launch_pdl(f8::quantize_blocks_kernel<float>, dim3(grid), dim3(256), 0, st, a, units);
+    const unsigned steps = (unsigned)(per * std::min(step, a.n - r)), grid = f8_step_ctas(steps);
+    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, dim3(grid), dim3(256), 0, st, a, steps)
+                            : launch_pdl(f8::quantize_blocks_kernel<float>, dim3(grid), dim3(256), 0, st, a, steps);
     if (e != cudaSuccess) return CSA_ERR_CUDA;
     CSA_CHECK_LAUNCH();
     if (a.n - r <= step) break;
@@ -1498,8 +1518,8 @@ template <int BN, int kStages>
 csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8GemmArgs& a, cudaStream_t st) {
   using Cfg = F8GemmCfg<BN, kStages>;
   auto k = gemm_f8_kernel<BN, kStages>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM) != cudaSuccess)
-    return CSA_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!allow_smem(k, Cfg::SMEM, smem_set)) return CSA_ERR_CUDA;
   const TcGemmArgs& g = a.g;
   const int tiles = ((g.M + Cfg::BM - 1) / Cfg::BM) * ((g.N + BN - 1) / BN) * g.k_split;
   const int grid = tiles < sm_count() ? tiles : sm_count();
@@ -1616,9 +1636,8 @@ csa_status launch_mqa_f8(const csa_dims* d, const MqaF8Args& a, void* ws, cudaSt
     const size_t rhs = (size_t)a.rows * a.nh * t.splits;
     t.part_o = static_cast<float*>(ws);
     t.part_lse = t.splits > 1 ? reinterpret_cast<float*>(at(ws, align_up(rhs * mqaf8::kC * 4))) : nullptr;
-    if (cudaFuncSetAttribute(mqa_f8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mqaf8::kSmem) !=
-        cudaSuccess)
-      return CSA_ERR_CUDA;
+    static std::atomic<uint64_t> smem_set{0};
+    if (!allow_smem(mqa_f8_tc_kernel, mqaf8::kSmem, smem_set)) return CSA_ERR_CUDA;
     const long long items = (long long)a.rows * (a.nh / mqaf8::kHeads) * t.splits;
     if (items > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
     const int grid = items < sm_count() ? (int)items : sm_count();
@@ -1704,17 +1723,17 @@ csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, c
   f8::DequantArgs a;
   a.codes = static_cast<const uint8_t*>(codes); a.ld_codes = ld_codes; a.scales = static_cast<const uint8_t*>(scales);
   a.ld_scales = ld_scales; a.rows = rows; a.n_slots = n_slots; a.X = X; a.ld = ld; a.w = w;
-  a.block_units = (block ? block : w) / f8::kUnit;
-  // threads are numbered in 32 bits: more than that many in several launches
-  const long long per = w / f8::kUnit;
+  a.block = block ? block : w;
+  // warp steps are numbered in 32 bits: more than that many in several launches
+  const long long per = f8_steps_per_row(dtype, w);
   const int step = (int)std::max(1ll, std::min<long long>(n, (1ll << 30) / per));
   for (int r = 0; r < n; r += step) {
     a.row0 = r;
-    const unsigned units = (unsigned)(per * std::min(step, n - r)), grid = (units + 255) / 256;
+    const unsigned steps = (unsigned)(per * std::min(step, n - r)), grid = f8_step_ctas(steps);
     const cudaError_t e =
         dtype == CSA_BF16
-            ? launch_pdl(f8::dequantize_kernel<bf16>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, units)
-            : launch_pdl(f8::dequantize_kernel<float>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, units);
+            ? launch_pdl(f8::dequantize_kernel<bf16>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, steps)
+            : launch_pdl(f8::dequantize_kernel<float>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, steps);
     if (e != cudaSuccess) return CSA_ERR_CUDA;
     CSA_CHECK_LAUNCH();
     if (n - r <= step) break;

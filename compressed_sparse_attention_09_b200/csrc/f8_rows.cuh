@@ -14,9 +14,10 @@
 // stored as the NaN code and leaves the block's scale alone; a block without
 // a finite non-zero value gets byte 0.
 //
-// All three kernels are one pass over HBM: a thread holds 16 consecutive
-// values (a 16-byte store of codes) in registers between the maximum and the
-// conversion, so each value is read once.
+// All kernels are one pass over HBM: a lane holds 16-byte vectors of values
+// (8 bf16 or 4 fp32) in registers between the maximum and the conversion, so
+// each value is read once, and the lanes of a warp take neighbouring vectors,
+// so that every load and store instruction covers whole 128-byte lines.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -26,8 +27,9 @@
 namespace csa {
 namespace f8 {
 
-constexpr int kUnit = 16;    // values per thread: one 16-byte store of codes
+constexpr int kUnit = 16;    // row widths are multiples of this
 constexpr int kBlock = 128;  // values per scale of a blocked row
+constexpr int kSteps = 4;    // warp steps (32 vectors each) that a thread keeps in flight
 
 // Scale byte of a block whose largest finite magnitude has these fp32 bits.
 __device__ __forceinline__ int scale_byte(uint32_t amax_bits) {
@@ -39,6 +41,30 @@ __device__ __forceinline__ float inv_scale(int b) { return __uint_as_float((uint
 // 2^(b - 127); byte 0 is the subnormal 2^-127, byte 255 is NaN
 __device__ __forceinline__ float scale_value(uint32_t b) {
   return b == 0 ? __uint_as_float(0x00400000u) : b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 23);
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Packed fp32 pairs (one instruction for two values).
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 upk2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Two E4M3 codes (low and high byte of v) as fp32.
@@ -54,66 +80,56 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
   return v;
 }
 
-// 16 consecutive values of a row, as loaded (streamed: read once).
-template <typename T> struct Unit {
-  static constexpr int kVecs = kUnit / Vec16<T>::V;
-  uint4 v[kVecs];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+// One 16-byte vector of a row's values.
+template <typename T> struct Vec {
+  static constexpr int V = Vec16<T>::V;
+  uint4 v;
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (V == 4) return __uint_as_float(reinterpret_cast<const uint32_t*>(&v)[e]);
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[e >> 1];
+    return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);   // a bf16 is the upper half of its fp32
   }
-  __device__ __forceinline__ void load_shared(const T* p) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = *(reinterpret_cast<const uint4*>(p) + i);
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ float at(int e) const { return to_f32(reinterpret_cast<const T*>(v)[e]); }
-  // fp32 bits of the largest finite magnitude
+  // fp32 bits of the largest magnitude, NaN values aside
   __device__ __forceinline__ uint32_t amax() const {
+    if constexpr (V == 8) {
+      __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162*>(&v)[q]));
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+      return max(w << 16, w & 0xFFFF0000u);
+    }
+    return __float_as_uint(fmaxf(fmaxf(fabsf(at(0)), fabsf(at(1))), fmaxf(fabsf(at(2)), fabsf(at(V - 1)))));
+  }
+  // the same, infinite values aside too (for blocks that hold one)
+  __device__ __forceinline__ uint32_t amax_finite() const {
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e) {
+    for (int e = 0; e < V; ++e) {
       const uint32_t b = __float_as_uint(at(e)) & 0x7FFFFFFFu;
       m = max(m, b < 0x7F800000u ? b : 0u);
     }
     return m;
   }
-  __device__ __forceinline__ uint4 encode(float inv) const {
-    uint32_t w[4];
+  // its V codes, to a V-byte aligned address; `inf`: the block holds infinite
+  // values, which become NaN codes (a NaN value converts to one by itself)
+  __device__ __forceinline__ void encode_to(uint8_t* dst, float inv, bool inf) const {
+    uint32_t w[V / 4];
+    const uint64_t inv2 = pk2(inv, inv);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = at(4 * q + e);
-        x[e] = fabsf(a) < INFINITY ? a * inv : NAN;
+    for (int q = 0; q < V / 4; ++q) {
+      float2 x = upk2(mul2(pk2(at(4 * q), at(4 * q + 1)), inv2)), y = upk2(mul2(pk2(at(4 * q + 2), at(4 * q + 3)), inv2));
+      if (inf) {
+        x.x = fabsf(x.x) < INFINITY ? x.x : NAN;
+        x.y = fabsf(x.y) < INFINITY ? x.y : NAN;
+        y.x = fabsf(y.x) < INFINITY ? y.x : NAN;
+        y.y = fabsf(y.y) < INFINITY ? y.y : NAN;
       }
-      w[q] = f32x2_to_e4m3(x[0], x[1]) | (f32x2_to_e4m3(x[2], x[3]) << 16);
+      w[q] = f32x2_to_e4m3(x.x, x.y) | (f32x2_to_e4m3(y.x, y.y) << 16);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
 };
-
-// 16 codes times one factor, as 16 values of T.
-template <typename T>
-__device__ __forceinline__ void decode_unit(const uint4& c, float scale, T* dst) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < kUnit / Vec16<T>::V; ++i) {
-    Vec16<T> o;
-#pragma unroll
-    for (int e = 0; e < Vec16<T>::V; e += 2) {
-      const int k = i * Vec16<T>::V + e;
-      const float2 f = e4m3x2_to_f32((uint16_t)(w[k >> 2] >> (8 * (k & 3))));
-      o.e[e] = from_f32<T>(f.x * scale);
-      o.e[e + 1] = from_f32<T>(f.y * scale);
-    }
-    __stcs(reinterpret_cast<uint4*>(dst) + i, o.u);
-  }
-}
 
 struct QuantArgs {
   const void* X; long long ld;            // [n, w] values
@@ -124,107 +140,148 @@ struct QuantArgs {
   int row0;                               // first row of this launch
 };
 
-__device__ __forceinline__ long long quant_slot(const QuantArgs& a, int row, bool teller) {
-  if (!a.slots) return row;
-  const int s = __ldg(a.slots + row);
-  if (s >= 0 && s < a.n_slots) return s;
-  if (s != -1 && teller) flag_status(kStatusBadIndex);
+// The destination row of source row `row`, given its slot (loaded ahead; the
+// row itself where there are no slots); -1: not stored.
+__device__ __forceinline__ int load_slot(const QuantArgs& a, int row) { return a.slots ? __ldg(a.slots + row) : row; }
+__device__ __forceinline__ long long quant_slot(const QuantArgs& a, int slot, bool teller) {
+  if (!a.slots || (slot >= 0 && slot < a.n_slots)) return slot;
+  if (slot != -1 && teller) flag_status(kStatusBadIndex);
   return -1;
 }
 
-// Blocks of 128: eight neighbouring threads share a block.  A row takes
-// 8 * ceil(w / 128) threads, so that a block never crosses a warp.
+// Blocks of 128: a warp step is 32 vectors of a row (two blocks of bf16, one
+// of fp32), so that a block never crosses a step; a warp takes kSteps steps.
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a, unsigned units) {
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a, unsigned steps) {
+  constexpr int V = Vec<T>::V, kStep = 32 * V;
   pdl_prologue_done();
-  const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;
-  const unsigned per = 8u * (unsigned)((a.w + kBlock - 1) / kBlock);
-  const unsigned r = i / per, u = i - r * per;
-  const bool some = i < units && (int)(u * kUnit) < a.w;
-  const int row = a.row0 + (int)r;
-  Unit<T> x;
-  if (some) x.load(static_cast<const T*>(a.X) + (long long)row * a.ld + u * kUnit);
-  else x.clear();
-  uint32_t m = x.amax();
+  const int lane = threadIdx.x & 31;
+  const unsigned s0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kSteps;
+  const unsigned per = (unsigned)((a.w + kStep - 1) / kStep);   // steps per row
+  Vec<T> x[kSteps];
+  int slot[kSteps], col[kSteps];
 #pragma unroll
-  for (int off = 4; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (!some) return;
-  const long long dst = quant_slot(a, row, u == 0);
-  if (dst < 0) return;
-  const int b = scale_byte(m);
-  *reinterpret_cast<uint4*>(a.codes + dst * a.ld_codes + u * kUnit) = x.encode(inv_scale(b));
-  if ((u & 7) == 0) a.scales[dst * a.ld_scales + (u >> 3)] = (uint8_t)b;
+  for (int k = 0; k < kSteps; ++k) {
+    const unsigned s = s0 + k, r = s / per;
+    const int row = a.row0 + (int)r;
+    col[k] = (int)(s - r * per) * kStep + V * lane;
+    if (s >= steps) col[k] = a.w;
+    x[k].v = make_uint4(0, 0, 0, 0);
+    slot[k] = -1;
+    if (col[k] < a.w) {
+      x[k].v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + (long long)row * a.ld + col[k]));
+      slot[k] = load_slot(a, row);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    uint32_t m = x[k].amax();
+#pragma unroll
+    for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const bool inf = m >= kInfBits;
+    if (__any_sync(0xffffffffu, inf)) {
+      m = x[k].amax_finite();
+#pragma unroll
+      for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+    if (col[k] >= a.w) continue;
+    const long long dst = quant_slot(a, slot[k], col[k] == 0);
+    if (dst < 0) continue;
+    const int b = scale_byte(m);
+    x[k].encode_to(a.codes + dst * a.ld_codes + col[k], inv_scale(b), inf);
+    if (col[k] % kBlock == 0) a.scales[dst * a.ld_scales + col[k] / kBlock] = (uint8_t)b;
+  }
 }
 
-// One scale for the whole row: one warp per row.  Rows of up to 1024 values
-// stay in registers; longer ones are read twice (the second time from L2).
+// One scale for the whole row: one warp per row.  Rows of up to kSteps steps
+// (1024 bf16, 512 fp32 values) stay in registers; longer ones are read twice
+// (the second time from L2).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantArgs a) {
+  constexpr int V = Vec<T>::V, kStep = 32 * V;
   pdl_prologue_done();
   const int lane = threadIdx.x & 31;
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (r >= a.n) return;
-  const int row = (int)r, units = a.w / kUnit;
-  const T* src = static_cast<const T*>(a.X) + (long long)row * a.ld;
-  Unit<T> x[2];
-  uint32_t m = 0;
-  for (int u0 = 0; u0 < units; u0 += 64) {
+  const int row = (int)r;
+  const T* src = static_cast<const T*>(a.X) + (long long)row * a.ld + V * lane;
+  Vec<T> x[kSteps];
+  const int slot = load_slot(a, row);
+  auto row_max = [&](bool finite) {
+    uint32_t m = 0;
+    for (int c0 = 0; c0 < a.w; c0 += kSteps * kStep) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int u = u0 + 32 * k + lane;
-      if (u < units) x[k].load(src + u * kUnit);
-      else x[k].clear();
+      for (int k = 0; k < kSteps; ++k) {
+        x[k].v = make_uint4(0, 0, 0, 0);
+        if (c0 + k * kStep + V * lane < a.w) x[k].v = __ldcs(reinterpret_cast<const uint4*>(src + c0 + k * kStep));
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) m = max(m, finite ? x[k].amax_finite() : x[k].amax());
     }
-    m = max(m, max(x[0].amax(), x[1].amax()));
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  const long long dst = quant_slot(a, row, lane == 0);
+    return __reduce_max_sync(0xffffffffu, m);
+  };
+  uint32_t m = row_max(false);
+  const bool inf = m >= kInfBits;
+  if (inf) m = row_max(true);
+  const long long dst = quant_slot(a, slot, lane == 0);
   if (dst < 0) return;
   const int b = scale_byte(m);
   const float inv = inv_scale(b);
-  for (int u0 = 0; u0 < units; u0 += 64) {
+  uint8_t* out = a.codes + dst * a.ld_codes + V * lane;
+  const bool kept = a.w <= kSteps * kStep;
+  for (int c0 = 0; c0 < a.w; c0 += kSteps * kStep) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int u = u0 + 32 * k + lane;
-      if (u >= units) continue;
-      if (units > 64) x[k].load(src + u * kUnit);
-      *reinterpret_cast<uint4*>(a.codes + dst * a.ld_codes + u * kUnit) = x[k].encode(inv);
+    for (int k = 0; k < kSteps; ++k) {
+      if (c0 + k * kStep + V * lane >= a.w) continue;
+      if (!kept) x[k].v = __ldcs(reinterpret_cast<const uint4*>(src + c0 + k * kStep));
+      x[k].encode_to(out + c0 + k * kStep, inv, inf);
     }
   }
   if (lane == 0) a.scales[dst * a.ld_scales] = (uint8_t)b;
 }
 
 // A matrix [N, K] with one scale for each 128 x 128 values: one CTA per
-// square, a thread holding 16 columns of four rows.
+// square, a warp 16 of its rows (32 of a square's columns at a time per
+// 128-byte line of codes).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_squares_kernel(const T* W, long long ld, int N, int K, uint8_t* codes,
                                                                long long ld_codes, uint8_t* scales,
                                                                long long ld_scales) {
-  __shared__ uint32_t top;
+  constexpr int V = Vec<T>::V, kLanes = kBlock / V, kRows = 256 / kLanes, kPasses = kBlock / kRows;
+  __shared__ uint32_t top[2];   // largest magnitude; largest finite one, where that is infinite
   pdl_prologue_done();
-  const int k0 = blockIdx.x * kBlock, u = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int k = blockIdx.x * kBlock + V * (threadIdx.x % kLanes), r0 = threadIdx.x / kLanes;
   for (int by = blockIdx.y; by * kBlock < N; by += gridDim.y) {
-    if (threadIdx.x == 0) top = 0;
+    if (threadIdx.x < 2) top[threadIdx.x] = 0;
     __syncthreads();
-    Unit<T> x[4];
+    Vec<T> x[kPasses];
     uint32_t m = 0;
-    const int k = k0 + u * kUnit;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = by * kBlock + r0 + 32 * i;
-      if (r < N && k < K) x[i].load(W + (long long)r * ld + k);
-      else x[i].clear();
-      m = max(m, x[i].amax());
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = by * kBlock + r0 + kRows * i;
+      x[i].v = make_uint4(0, 0, 0, 0);
+      if (r < N && k < K) x[i].v = __ldcs(reinterpret_cast<const uint4*>(W + (long long)r * ld + k));
     }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) m = max(m, x[i].amax());
     m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) atomicMax(&top, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(&top[0], m);
     __syncthreads();
-    const int b = scale_byte(top);
+    const bool inf = top[0] >= kInfBits;
+    if (inf) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) m = max(m, x[i].amax_finite());
+      m = __reduce_max_sync(0xffffffffu, m);
+      if ((threadIdx.x & 31) == 0) atomicMax(&top[1], m);
+      __syncthreads();
+    }
+    const int b = scale_byte(top[inf ? 1 : 0]);
     const float inv = inv_scale(b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = by * kBlock + r0 + 32 * i;
-      if (r < N && k < K) *reinterpret_cast<uint4*>(codes + (long long)r * ld_codes + k) = x[i].encode(inv);
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = by * kBlock + r0 + kRows * i;
+      if (r < N && k < K) x[i].encode_to(codes + (long long)r * ld_codes + k, inv, inf);
     }
     if (threadIdx.x == 0) scales[(long long)by * ld_scales + blockIdx.x] = (uint8_t)b;
     __syncthreads();
@@ -236,32 +293,64 @@ struct DequantArgs {
   const uint8_t* scales; long long ld_scales;
   const int* rows; int n_slots;           // source row of output row r (NULL: r); -1: zeros
   void* X; long long ld;
-  int w, block_units;                     // 16-value units of a row's scale block
+  int w, block;                           // values of a row; per scale
   int row0;
 };
 
-// Read back: one thread per 16 codes.
+// Read back: a warp step is 32 output vectors of a row; a warp takes kSteps.
 template <typename T>
-__global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned units) {
+__global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned steps) {
+  constexpr int V = Vec<T>::V, kStep = 32 * V;
   pdl_prologue_done();
-  const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= units) return;
-  const unsigned per = (unsigned)(a.w / kUnit);
-  const unsigned r = i / per, u = i - r * per;
-  const int row = a.row0 + (int)r;
-  long long src = row;
-  if (a.rows) {
-    const int s = __ldg(a.rows + row);
-    src = s >= 0 && s < a.n_slots ? s : -1;
-    if (src < 0 && s != -1 && u == 0) flag_status(kStatusBadIndex);
+  const int lane = threadIdx.x & 31;
+  const unsigned s0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kSteps;
+  const unsigned per = (unsigned)((a.w + kStep - 1) / kStep);   // steps per row
+  int row[kSteps], col[kSteps];
+  long long src[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const unsigned s = s0 + k, r = s / per;
+    row[k] = a.row0 + (int)r;
+    col[k] = s < steps ? (int)(s - r * per) * kStep + V * lane : a.w;
+    src[k] = row[k];
+    if (a.rows && s < steps) {
+      const int at = __ldg(a.rows + row[k]);
+      src[k] = at >= 0 && at < a.n_slots ? at : -1;
+      if (src[k] < 0 && at != -1 && col[k] == 0) flag_status(kStatusBadIndex);
+    }
   }
-  uint4 c = make_uint4(0, 0, 0, 0);
-  float scale = 0.f;
-  if (src >= 0) {
-    c = __ldg(reinterpret_cast<const uint4*>(a.codes + src * a.ld_codes) + u);
-    scale = scale_value(__ldg(a.scales + src * a.ld_scales + u / (unsigned)a.block_units));
+  uint32_t c[kSteps][V / 4];
+  uint32_t b[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) c[k][q] = 0;
+    b[k] = 127;
+    if (col[k] < a.w && src[k] >= 0) {
+      const uint8_t* p = a.codes + src[k] * a.ld_codes + col[k];
+      if constexpr (V == 8) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        c[k][0] = u.x;
+        c[k][1] = u.y;
+      } else {
+        c[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      }
+      b[k] = __ldg(a.scales + src[k] * a.ld_scales + col[k] / a.block);
+    }
   }
-  decode_unit<T>(c, scale, static_cast<T*>(a.X) + (long long)row * a.ld + u * kUnit);
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    if (col[k] >= a.w) continue;
+    const float scale = scale_value(b[k]);
+    Vec16<T> o;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 f = e4m3x2_to_f32((uint16_t)(c[k][e >> 2] >> (8 * (e & 3))));
+      o.e[e] = from_f32<T>(f.x * scale);
+      o.e[e + 1] = from_f32<T>(f.y * scale);
+    }
+    __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.X) + (long long)row[k] * a.ld + col[k]), o.u);
+  }
 }
 
 }  // namespace f8

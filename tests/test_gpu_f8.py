@@ -37,6 +37,10 @@ def test_quantize_bit_for_bit(n, w, block, dtype):
     x = rows_of(rng, n, w, dtype)
     if n > 4:
         x[4, 1], x[4, w - 1] = float("inf"), float("nan")
+        if n > 5:
+            x[5, w // 2] = float("nan")
+        if n > 6:
+            x[6, :] = float("-inf")
     nb = -(-w // block) if block else 1
     src = torch.zeros(n, w + 16, dtype=dtype, device=DEV)      # strided source and destinations
     src[:, :w] = x.to(DEV)
