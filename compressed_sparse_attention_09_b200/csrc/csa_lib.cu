@@ -1465,12 +1465,23 @@ namespace {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Warp steps of a row (32 16-byte vectors each), and the CTAs of so many steps.
-long long f8_steps_per_row(int dtype, int w) {
-  const int step = 32 * (dtype == CSA_BF16 ? 8 : 4);
-  return (w + step - 1) / step;
+// How the row kernels walk over rows row0 .. n - 1 of w values (f8::Walk), as
+// many of them as 32-bit warp numbers allow; the next launch starts at next.
+f8::Walk f8_walk(int dtype, int w, int row0, int n, int* next) {
+  const int step = 32 * (dtype == CSA_BF16 ? 8 : 4), per = (w + step - 1) / step;
+  f8::Walk k;
+  const bool along = per >= f8::kSteps;   // kSteps steps of one row, or one step of kSteps rows
+  k.cols = along ? (per + f8::kSteps - 1) / f8::kSteps : per;
+  k.row_step = along ? 0 : 1;
+  k.col_step = along ? 1 : 0;
+  const long long most = (1ll << 30) / k.cols * (along ? 1 : f8::kSteps);
+  k.row0 = row0;
+  k.n = (int)std::min<long long>(n, row0 + most);
+  const long long rows = k.n - row0, groups = along ? rows : (rows + f8::kSteps - 1) / f8::kSteps;
+  k.warps = (unsigned)(groups * k.cols);
+  *next = k.n;
+  return k;
 }
-unsigned f8_step_ctas(unsigned steps) { return (steps + 8 * f8::kSteps - 1) / (8 * f8::kSteps); }
 
 csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t st) {
   CSA_RANGE("quantize_f8");
@@ -1484,17 +1495,13 @@ csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t s
     CSA_CHECK_LAUNCH();
     return CSA_OK;
   }
-  // warp steps are numbered in 32 bits: more than that many in several launches
-  const long long per = f8_steps_per_row(dtype, a.w);
-  const int step = (int)std::max(1ll, std::min<long long>(a.n, (1ll << 30) / per));
-  for (int r = 0; r < a.n; r += step) {
-    a.row0 = r;
-    const unsigned steps = (unsigned)(per * std::min(step, a.n - r)), grid = f8_step_ctas(steps);
-    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, dim3(grid), dim3(256), 0, st, a, steps)
-                            : launch_pdl(f8::quantize_blocks_kernel<float>, dim3(grid), dim3(256), 0, st, a, steps);
+  for (int r = 0; r < a.n;) {
+    a.walk = f8_walk(dtype, a.w, r, a.n, &r);
+    const dim3 grid((a.walk.warps + 7) / 8);
+    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, grid, dim3(256), 0, st, a)
+                            : launch_pdl(f8::quantize_blocks_kernel<float>, grid, dim3(256), 0, st, a);
     if (e != cudaSuccess) return CSA_ERR_CUDA;
     CSA_CHECK_LAUNCH();
-    if (a.n - r <= step) break;
   }
   return CSA_OK;
 }
@@ -1705,7 +1712,6 @@ csa_status csa_quantize_f8(int dtype, const void* X, long long ld, int n, int w,
   f8::QuantArgs a;
   a.X = X; a.ld = ld; a.slots = slots; a.n_slots = n_slots; a.codes = static_cast<uint8_t*>(codes);
   a.ld_codes = ld_codes; a.scales = static_cast<uint8_t*>(scales); a.ld_scales = ld_scales; a.n = n; a.w = w;
-  a.row0 = 0;
   return launch_quantize(dtype, a, block, (cudaStream_t)stream);
 }
 
@@ -1724,19 +1730,14 @@ csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, c
   a.codes = static_cast<const uint8_t*>(codes); a.ld_codes = ld_codes; a.scales = static_cast<const uint8_t*>(scales);
   a.ld_scales = ld_scales; a.rows = rows; a.n_slots = n_slots; a.X = X; a.ld = ld; a.w = w;
   a.block = block ? block : w;
-  // warp steps are numbered in 32 bits: more than that many in several launches
-  const long long per = f8_steps_per_row(dtype, w);
-  const int step = (int)std::max(1ll, std::min<long long>(n, (1ll << 30) / per));
-  for (int r = 0; r < n; r += step) {
-    a.row0 = r;
-    const unsigned steps = (unsigned)(per * std::min(step, n - r)), grid = f8_step_ctas(steps);
+  for (int r = 0; r < n;) {
+    a.walk = f8_walk(dtype, w, r, n, &r);
+    const dim3 grid((a.walk.warps + 7) / 8);
     const cudaError_t e =
-        dtype == CSA_BF16
-            ? launch_pdl(f8::dequantize_kernel<bf16>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, steps)
-            : launch_pdl(f8::dequantize_kernel<float>, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a, steps);
+        dtype == CSA_BF16 ? launch_pdl(f8::dequantize_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, a)
+                          : launch_pdl(f8::dequantize_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, a);
     if (e != cudaSuccess) return CSA_ERR_CUDA;
     CSA_CHECK_LAUNCH();
-    if (n - r <= step) break;
   }
   return CSA_OK;
 }

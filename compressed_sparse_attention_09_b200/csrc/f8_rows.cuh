@@ -73,11 +73,16 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
-// Two fp32 values to E4M3 codes, `lo` in the low byte.
-__device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
-  uint16_t v;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
-  return v;
+// Four fp32 values to E4M3 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3(float2 x, float2 y) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(w)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return w;
 }
 
 // One 16-byte vector of a row's values.
@@ -124,11 +129,22 @@ template <typename T> struct Vec {
         y.x = fabsf(y.x) < INFINITY ? y.x : NAN;
         y.y = fabsf(y.y) < INFINITY ? y.y : NAN;
       }
-      w[q] = f32x2_to_e4m3(x.x, x.y) | (f32x2_to_e4m3(y.x, y.y) << 16);
+      w[q] = f32x4_to_e4m3(x, y);
     }
     if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
+};
+
+// How warps walk over rows of `per` steps (32 vectors each): a warp's kSteps
+// steps are kSteps neighbours in one row where rows are long enough, else the
+// same step of kSteps rows, so that each is the last one plus a constant.
+// Work is numbered warp by warp, `cols` warps to a row (or group of rows).
+struct Walk {
+  int cols, row_step, col_step;   // col_step in steps
+  unsigned warps;                 // of this launch
+  int row0;                       // its first row
+  int n;                          // end of its rows
 };
 
 struct QuantArgs {
@@ -137,40 +153,52 @@ struct QuantArgs {
   uint8_t* codes; long long ld_codes;
   uint8_t* scales; long long ld_scales;
   int n, w;
-  int row0;                               // first row of this launch
+  Walk walk;
 };
 
 // The destination row of source row `row`, given its slot (loaded ahead; the
 // row itself where there are no slots); -1: not stored.
 __device__ __forceinline__ int load_slot(const QuantArgs& a, int row) { return a.slots ? __ldg(a.slots + row) : row; }
 __device__ __forceinline__ long long quant_slot(const QuantArgs& a, int slot, bool teller) {
-  if (!a.slots || (slot >= 0 && slot < a.n_slots)) return slot;
+  if (slot >= 0 && (!a.slots || slot < a.n_slots)) return slot;
   if (slot != -1 && teller) flag_status(kStatusBadIndex);
   return -1;
 }
 
+// Row and column (of this lane) of a warp's first step; false: no such warp.
+template <int V>
+__device__ __forceinline__ bool walk_start(const Walk& w, int& row, int& col) {
+  const unsigned i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (i >= w.warps) return false;
+  const unsigned r = i / (unsigned)w.cols, c = i - r * (unsigned)w.cols;
+  row = w.row0 + (int)r * (w.row_step ? kSteps : 1);
+  col = ((int)c * (w.row_step ? 1 : kSteps) * 32 + (int)(threadIdx.x & 31)) * V;
+  return true;
+}
+
 // Blocks of 128: a warp step is 32 vectors of a row (two blocks of bf16, one
 // of fp32), so that a block never crosses a step; a warp takes kSteps steps.
+// Bound by issue slots before HBM when each step looked up its own row (147
+// instructions a step, 23 us for 8192 x 4096 bf16 against 15 us of traffic);
+// hence the constant strides and the packed arithmetic.
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a, unsigned steps) {
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
   constexpr int V = Vec<T>::V, kStep = 32 * V;
   pdl_prologue_done();
-  const int lane = threadIdx.x & 31;
-  const unsigned s0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kSteps;
-  const unsigned per = (unsigned)((a.w + kStep - 1) / kStep);   // steps per row
+  int row0, col0;
+  if (!walk_start<V>(a.walk, row0, col0)) return;
+  const int dr = a.walk.row_step, dc = a.walk.col_step * kStep;
+  const T* src = static_cast<const T*>(a.X) + (long long)row0 * a.ld + col0;
+  const long long ds = dr * a.ld + dc;
   Vec<T> x[kSteps];
-  int slot[kSteps], col[kSteps];
+  int slot[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const unsigned s = s0 + k, r = s / per;
-    const int row = a.row0 + (int)r;
-    col[k] = (int)(s - r * per) * kStep + V * lane;
-    if (s >= steps) col[k] = a.w;
     x[k].v = make_uint4(0, 0, 0, 0);
     slot[k] = -1;
-    if (col[k] < a.w) {
-      x[k].v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + (long long)row * a.ld + col[k]));
-      slot[k] = load_slot(a, row);
+    if (row0 + k * dr < a.walk.n && col0 + k * dc < a.w) {
+      x[k].v = __ldcs(reinterpret_cast<const uint4*>(src + k * ds));
+      slot[k] = load_slot(a, row0 + k * dr);
     }
   }
 #pragma unroll
@@ -184,12 +212,12 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a, unsig
 #pragma unroll
       for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     }
-    if (col[k] >= a.w) continue;
-    const long long dst = quant_slot(a, slot[k], col[k] == 0);
+    const int col = col0 + k * dc;
+    const long long dst = quant_slot(a, slot[k], col == 0);
     if (dst < 0) continue;
     const int b = scale_byte(m);
-    x[k].encode_to(a.codes + dst * a.ld_codes + col[k], inv_scale(b), inf);
-    if (col[k] % kBlock == 0) a.scales[dst * a.ld_scales + col[k] / kBlock] = (uint8_t)b;
+    x[k].encode_to(a.codes + dst * a.ld_codes + col, inv_scale(b), inf);
+    if ((col & (kBlock - 1)) == 0) a.scales[dst * a.ld_scales + (col >> 7)] = (uint8_t)b;
   }
 }
 
@@ -294,29 +322,28 @@ struct DequantArgs {
   const int* rows; int n_slots;           // source row of output row r (NULL: r); -1: zeros
   void* X; long long ld;
   int w, block;                           // values of a row; per scale
-  int row0;
+  Walk walk;
 };
 
 // Read back: a warp step is 32 output vectors of a row; a warp takes kSteps.
 template <typename T>
-__global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned steps) {
+__global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a) {
   constexpr int V = Vec<T>::V, kStep = 32 * V;
   pdl_prologue_done();
-  const int lane = threadIdx.x & 31;
-  const unsigned s0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kSteps;
-  const unsigned per = (unsigned)((a.w + kStep - 1) / kStep);   // steps per row
-  int row[kSteps], col[kSteps];
-  long long src[kSteps];
+  int row0, col0;
+  if (!walk_start<V>(a.walk, row0, col0)) return;
+  const int dr = a.walk.row_step, dc = a.walk.col_step * kStep;
+  int src[kSteps];
+  bool some[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const unsigned s = s0 + k, r = s / per;
-    row[k] = a.row0 + (int)r;
-    col[k] = s < steps ? (int)(s - r * per) * kStep + V * lane : a.w;
-    src[k] = row[k];
-    if (a.rows && s < steps) {
-      const int at = __ldg(a.rows + row[k]);
+    const int row = row0 + k * dr;
+    some[k] = row < a.walk.n && col0 + k * dc < a.w;
+    src[k] = row;
+    if (a.rows && some[k]) {
+      const int at = __ldg(a.rows + row);
       src[k] = at >= 0 && at < a.n_slots ? at : -1;
-      if (src[k] < 0 && at != -1 && col[k] == 0) flag_status(kStatusBadIndex);
+      if (src[k] < 0 && at != -1 && col0 + k * dc == 0) flag_status(kStatusBadIndex);
     }
   }
   uint32_t c[kSteps][V / 4];
@@ -326,8 +353,9 @@ __global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned
 #pragma unroll
     for (int q = 0; q < V / 4; ++q) c[k][q] = 0;
     b[k] = 127;
-    if (col[k] < a.w && src[k] >= 0) {
-      const uint8_t* p = a.codes + src[k] * a.ld_codes + col[k];
+    if (some[k] && src[k] >= 0) {
+      const int col = col0 + k * dc;
+      const uint8_t* p = a.codes + src[k] * a.ld_codes + col;
       if constexpr (V == 8) {
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
         c[k][0] = u.x;
@@ -335,12 +363,12 @@ __global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned
       } else {
         c[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
       }
-      b[k] = __ldg(a.scales + src[k] * a.ld_scales + col[k] / a.block);
+      b[k] = __ldg(a.scales + src[k] * a.ld_scales + (a.block == kBlock ? col >> 7 : 0));
     }
   }
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    if (col[k] >= a.w) continue;
+    if (!some[k]) continue;
     const float scale = scale_value(b[k]);
     Vec16<T> o;
 #pragma unroll
@@ -349,7 +377,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a, unsigned
       o.e[e] = from_f32<T>(f.x * scale);
       o.e[e + 1] = from_f32<T>(f.y * scale);
     }
-    __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.X) + (long long)row[k] * a.ld + col[k]), o.u);
+    __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.X) + (long long)(row0 + k * dr) * a.ld + col0 + k * dc), o.u);
   }
 }
 
