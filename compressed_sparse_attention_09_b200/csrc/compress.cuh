@@ -315,7 +315,7 @@ __device__ __forceinline__ void cache_append_cta(const AppendArgs& a, float* ki_
       const long long e = (long long)b * a.cap + i;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (8 * (lane + 32 * k) < c) x[k].encode_to(a.Ccodes + e * c + 8 * (lane + 32 * k), inv, inf);
+        if (8 * (lane + 32 * k) < c) x[k].encode_to<true>(a.Ccodes + e * c + 8 * (lane + 32 * k), inv);
       if (lane == 0) a.Cscale[e] = (uint8_t)sb;
     }
   }

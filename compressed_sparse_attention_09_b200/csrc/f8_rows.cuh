@@ -22,6 +22,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace csa {
@@ -115,15 +117,16 @@ template <typename T> struct Vec {
     }
     return m;
   }
-  // its V codes, to a V-byte aligned address; `inf`: the block holds infinite
-  // values, which become NaN codes (a NaN value converts to one by itself)
-  __device__ __forceinline__ void encode_to(uint8_t* dst, float inv, bool inf) const {
+  // its V codes, to a V-byte aligned address.  kInf: the block holds infinite
+  // values, which become NaN codes (a NaN value converts to one by itself).
+  template <bool kInf>
+  __device__ __forceinline__ void encode_to(uint8_t* dst, float inv) const {
     uint32_t w[V / 4];
     const uint64_t inv2 = pk2(inv, inv);
 #pragma unroll
     for (int q = 0; q < V / 4; ++q) {
       float2 x = upk2(mul2(pk2(at(4 * q), at(4 * q + 1)), inv2)), y = upk2(mul2(pk2(at(4 * q + 2), at(4 * q + 3)), inv2));
-      if (inf) {
+      if constexpr (kInf) {
         x.x = fabsf(x.x) < INFINITY ? x.x : NAN;
         x.y = fabsf(x.y) < INFINITY ? x.y : NAN;
         y.x = fabsf(y.x) < INFINITY ? y.x : NAN;
@@ -201,23 +204,28 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
       slot[k] = load_slot(a, row0 + k * dr);
     }
   }
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    uint32_t m = x[k].amax();
-#pragma unroll
-    for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const bool inf = m >= kInfBits;
-    if (__any_sync(0xffffffffu, inf)) {
+  // A step's codes and scales; kInf as for encode_to (rare, and then for the whole warp).
+  auto store = [&](auto inf, int k, uint32_t m) {
+    constexpr bool kInf = decltype(inf)::value;
+    if constexpr (kInf) {
       m = x[k].amax_finite();
 #pragma unroll
       for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     }
     const int col = col0 + k * dc;
     const long long dst = quant_slot(a, slot[k], col == 0);
-    if (dst < 0) continue;
+    if (dst < 0) return;
     const int b = scale_byte(m);
-    x[k].encode_to(a.codes + dst * a.ld_codes + col, inv_scale(b), inf);
+    x[k].template encode_to<kInf>(a.codes + dst * a.ld_codes + col, inv_scale(b));
     if ((col & (kBlock - 1)) == 0) a.scales[dst * a.ld_scales + (col >> 7)] = (uint8_t)b;
+  };
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    uint32_t m = x[k].amax();
+#pragma unroll
+    for (int off = kBlock / V / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (__any_sync(0xffffffffu, m >= kInfBits)) store(std::true_type{}, k, m);
+    else store(std::false_type{}, k, m);
   }
 }
 
@@ -257,14 +265,18 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantArgs a) {
   const float inv = inv_scale(b);
   uint8_t* out = a.codes + dst * a.ld_codes + V * lane;
   const bool kept = a.w <= kSteps * kStep;
-  for (int c0 = 0; c0 < a.w; c0 += kSteps * kStep) {
+  auto store = [&](auto inf) {
+    for (int c0 = 0; c0 < a.w; c0 += kSteps * kStep) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      if (c0 + k * kStep + V * lane >= a.w) continue;
-      if (!kept) x[k].v = __ldcs(reinterpret_cast<const uint4*>(src + c0 + k * kStep));
-      x[k].encode_to(out + c0 + k * kStep, inv, inf);
+      for (int k = 0; k < kSteps; ++k) {
+        if (c0 + k * kStep + V * lane >= a.w) continue;
+        if (!kept) x[k].v = __ldcs(reinterpret_cast<const uint4*>(src + c0 + k * kStep));
+        x[k].template encode_to<decltype(inf)::value>(out + c0 + k * kStep, inv);
+      }
     }
-  }
+  };
+  if (inf) store(std::true_type{});
+  else store(std::false_type{});
   if (lane == 0) a.scales[dst * a.ld_scales] = (uint8_t)b;
 }
 
@@ -309,7 +321,7 @@ __global__ void __launch_bounds__(256) quantize_squares_kernel(const T* W, long 
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int r = by * kBlock + r0 + kRows * i;
-      if (r < N && k < K) x[i].encode_to(codes + (long long)r * ld_codes + k, inv, inf);
+      if (r < N && k < K) x[i].template encode_to<true>(codes + (long long)r * ld_codes + k, inv);
     }
     if (threadIdx.x == 0) scales[(long long)by * ld_scales + blockIdx.x] = (uint8_t)b;
     __syncthreads();
