@@ -1521,10 +1521,10 @@ csa_status launch_quantize_squares(int dtype, const void* W, long long ld, int N
   return CSA_OK;
 }
 
-template <int BN, int kStages>
+template <int BN, int kGroups>
 csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8GemmArgs& a, cudaStream_t st) {
-  using Cfg = F8GemmCfg<BN, kStages>;
-  auto k = gemm_f8_kernel<BN, kStages>;
+  using Cfg = F8GemmCfg<BN, kGroups>;
+  auto k = gemm_f8_kernel<BN, kGroups>;
   static std::atomic<uint64_t> smem_set{0};
   if (!allow_smem(k, Cfg::SMEM, smem_set)) return CSA_ERR_CUDA;
   const TcGemmArgs& g = a.g;
@@ -1582,23 +1582,30 @@ csa_status launch_gemm_f8(const void* A, long long lda, const void* sa, long lon
     a.sb = rows_a;
     a.g.k_split = f8_gemm_splits(M, N, K);
     a.g.part = static_cast<float*>(ws);
-    return launch_f8_gemm<64, 8>(ta, tb, a, st);
+    return launch_f8_gemm<64, 2>(ta, tb, a, st);
   }
   a.g.M = M; a.g.N = N; a.g.transpose_out = 0;
   a.sa = rows_a;
   a.sb = rows_b;
   const int m_tiles = (M + 127) / 128;
-  auto cost = [&](int bn) {   // waves of tiles times a tile's length
+  // Waves of tiles times a tile's time, which is linear in its width: at
+  // K = 1536 4.0, 5.2 and 6.2 us for 128, 192 and 240 columns, that is bn + 80.
+  // 8192 x 40960 runs 635, 554 and 533 us with them; 1001 x 4160 x 4096 (264,
+  // 176 and 144 tiles) 27.3, 29.9 and 21.9 us.
+  auto cost = [&](int bn) {
     const long long tiles = (long long)m_tiles * ((N + bn - 1) / bn), sms = sm_count();
-    return (double)((tiles + sms - 1) / sms) * (double)bn;
+    return (tiles + sms - 1) / sms * (bn + 80);
   };
-  const int BN = cost(128) < cost(192) ? 128 : 192;
+  int BN = 240;
+  for (int bn : {192, 128})
+    if (cost(bn) < cost(BN)) BN = bn;
   if (!make_tmap_u8(&ta, A, K, M, (uint64_t)lda, 128, 128) || !make_tmap_u8(&tb, B, K, N, (uint64_t)ldb, 128, BN))
     return CSA_ERR_UNSUPPORTED;
   const int n_tiles = (N + BN - 1) / BN, sq = std::max(1, (int)lrint(sqrt((double)sm_count())));
   a.g.group_m = (size_t)M * K > ((size_t)32 << 20) ? std::max(sq, (sm_count() + n_tiles - 1) / n_tiles) : m_tiles;
   if (a.g.group_m > m_tiles) a.g.group_m = m_tiles;
-  return BN == 192 ? launch_f8_gemm<192, 5>(ta, tb, a, st) : launch_f8_gemm<128, 6>(ta, tb, a, st);
+  if (BN == 240) return launch_f8_gemm<240, 1>(ta, tb, a, st);
+  return BN == 192 ? launch_f8_gemm<192, 1>(ta, tb, a, st) : launch_f8_gemm<128, 1>(ta, tb, a, st);
 }
 
 // Whether the tensor-core MQA over 8-bit entries covers these dims.

@@ -19,13 +19,15 @@
 // Persistent, warp-specialised CTA (one per SM, 352 threads):
 //   warp 0      TMA producer: 128 x 128 codes of A and BN x 128 of B per
 //               stage, K-major with 128-byte swizzle;
-//   warp 1      owns TMEM; one thread copies scales to TMEM (tcgen05.cp),
-//               issues tcgen05.mma (M = 128, N = BN, K = 32) and commits;
+//   warp 1      owns TMEM; one thread issues tcgen05.mma (M = 128, N = BN,
+//               K = 32) and commits;
 //   warp 2      reads the scale bytes of four K blocks at a time into shared
-//               memory in the order tcgen05.cp takes, one group ahead;
+//               memory in the order tcgen05.cp takes and copies them to TMEM,
+//               ahead of the products;
 //   warps 3..10 epilogue, two per TMEM lane quarter.
 // Two accumulators (2 x BN columns) let a tile's epilogue overlap the next
-// tile's products; the other columns hold kSfBufs sets of scales.  Scale
+// tile's products; the other columns hold kSfBufs sets of scales (so BN is at
+// most 240).  Scale
 // buffer b (shared memory and TMEM) is refilled only after the last product
 // of the group that used it has completed (sf_empty).
 // Every wait is bounded, as in gemm_tc_kernel.
@@ -48,15 +50,18 @@ struct F8GemmArgs {
   ScaleRows sa, sb;
 };
 
-template <int BN, int kStages>
+// The ring holds kGroups groups of four stages (one scale group each), so that
+// a block's stage within its group is a constant of the unrolled code.
+template <int BN, int kGroups>
 struct F8GemmCfg {
+  static constexpr int kStages = 4 * kGroups;
   static constexpr int BM = kGemmRows, BK = 128;
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SFB_GROUPS = (BN + 127) / 128;           // 128-row groups of B's scales
   static constexpr int SF_BYTES = 512 * (1 + SFB_GROUPS);
   static constexpr int SF_COLS = 4 * (1 + SFB_GROUPS);
-  static constexpr int kSfBufs = 4;
+  static constexpr int kSfBufs = kGroups + 1;
   static constexpr int TMEM_COLS = 2 * BN + kSfBufs * SF_COLS <= 256 ? 256 : 512;
   static_assert(2 * BN + kSfBufs * SF_COLS <= 512, "accumulators and scales share TMEM");
   static constexpr int OUT_STAGE = kF8EpiWarps * 32 * 64;   // staging: 32 rows of 64 B per epilogue warp
@@ -96,26 +101,28 @@ __device__ __forceinline__ uint32_t r_sw64(int r, int u) { return (uint32_t)(r *
 struct F8Dest {
   uint8_t* p;      // row 0 of this warp's 32, column 0 of its range; NULL: general store
   long long pitch; // bytes between rows
-  int rows;        // rows in range
+  int rows, cols;  // in range
   int f32;
 };
 
-// Destination of rows r0 .. r0 + 31, columns c0 .. c0 + cols - 1.
+// Destination of rows r0 .. r0 + 31, columns c0 .. c0 + cols - 1 (those below
+// N that are stored in whole 16-byte pieces).
 __device__ __forceinline__ F8Dest f8_dest(const TcGemmArgs& g, int r0, int c0, int cols) {
   F8Dest d;
   d.p = nullptr;
   d.pitch = 0;
   d.f32 = 0;
   d.rows = min(32, g.M - r0);
-  if (g.transpose_out || g.k_split > 1 || c0 + cols > g.N) return d;
+  d.cols = min(cols, g.N - c0);
+  if (g.transpose_out || g.k_split > 1 || d.cols <= 0) return d;
 #pragma unroll 1
   for (int s = 0; s < g.out.nseg; ++s) {
     const OutSeg& sg = g.out.seg[s];
-    if (c0 < sg.col0 || c0 + cols > sg.col0 + sg.ncols) continue;
+    if (c0 < sg.col0 || c0 + d.cols > sg.col0 + sg.ncols) continue;
     const int es = sg.f32 ? 4 : 2;
     const long long pitch = sg.ld * es;
     uint8_t* p = static_cast<uint8_t*>(sg.ptr) + (long long)r0 * pitch + (long long)(c0 - sg.col0) * es;
-    if ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch) & 15) return d;
+    if ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch | (uintptr_t)(d.cols * es)) & 15) return d;
     d.p = p;
     d.pitch = pitch;
     d.f32 = sg.f32;
@@ -123,9 +130,9 @@ __device__ __forceinline__ F8Dest f8_dest(const TcGemmArgs& g, int r0, int c0, i
   return d;
 }
 
-// 64 bytes of each of this warp's rows (32 bf16 or 16 fp32 columns) through
-// the staging rows: eight rows per store instruction.
-__device__ __forceinline__ void f8_store_rows(const F8Dest& d, int byte0, const uint4* v, uint8_t* stage) {
+// 64 bytes of each of this warp's rows (32 bf16 or 16 fp32 columns; `bytes` of
+// them in range) through the staging rows: eight rows per store instruction.
+__device__ __forceinline__ void f8_store_rows(const F8Dest& d, int byte0, int bytes, const uint4* v, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(stage + r_sw64(lane, u)) = v[u];
@@ -135,38 +142,67 @@ __device__ __forceinline__ void f8_store_rows(const F8Dest& d, int byte0, const 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint4 x = *reinterpret_cast<const uint4*>(stage + r_sw64(r0 + 8 * i, u));
-    if (r0 + 8 * i < d.rows) *reinterpret_cast<uint4*>(p) = x;
+    if (r0 + 8 * i < d.rows && 16 * u < bytes) *reinterpret_cast<uint4*>(p) = x;
     p += 8 * d.pitch;
   }
   __syncwarp();
 }
 
-// The general store, out of line: it is long and rarely runs.
-__device__ __noinline__ void f8_store_general(const TcGemmArgs& g, int m_tiles, int mt, int sub, int ks, int c0, int acc_addr,
-                                              uint8_t* stage) {
-  float v0[32], v1[32];
-  sm100::tmem_ld_32x32b_x32(acc_addr, v0);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v1[j] = 0.f;
-  TcGemmArgs h = g;
-  h.N = min(g.N, c0 + 32);   // these 32 columns only
-  if (g.k_split > 1) {       // (the slice layout goes by the whole N)
-    const int r = mt * kGemmRows + sub * 32 + (threadIdx.x & 31);
-    const size_t ld = (size_t)m_tiles * kGemmRows;
-    float* dst = g.part + (size_t)ks * g.N * ld + r;
-    if (r < g.M)
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c0 + j < g.N) dst[(size_t)(c0 + j) * ld] = v0[j];
-    return;
+// Where one value per token (or per K slice's column) goes down a column: the
+// transposed and split forms.  Lanes are neighbouring output columns, so a
+// step j of the warp writes 64 or 128 contiguous bytes.
+struct F8Column {
+  uint8_t* p;       // value of accumulator column 0 of this lane's row; NULL: none
+  long long pitch;  // bytes from one accumulator column to the next
+  int f32;
+};
+__device__ __forceinline__ F8Column f8_column(const TcGemmArgs& g, int m_tiles, int r, int ks) {
+  F8Column d;
+  d.p = nullptr;
+  d.pitch = 0;
+  d.f32 = 1;
+  if (r >= g.M) return d;
+  if (g.k_split > 1) {   // this K slice's fp32 sum, column j of row r at part[(ks N + j) Mpad + r]
+    d.pitch = (long long)m_tiles * kGemmRows * 4;
+    d.p = reinterpret_cast<uint8_t*>(g.part) + (long long)ks * g.N * d.pitch + (long long)r * 4;
+    return d;
   }
-  gemm_store_cols64(h, m_tiles, mt, sub, ks, c0, v0, v1, stage);
+#pragma unroll 1
+  for (int s = 0; s < g.out.nseg; ++s) {
+    const OutSeg& sg = g.out.seg[s];
+    if (r < sg.col0 || r >= sg.col0 + sg.ncols) continue;
+    const int es = sg.f32 ? 4 : 2;
+    d.p = static_cast<uint8_t*>(sg.ptr) + (long long)(r - sg.col0) * es;
+    d.pitch = sg.ld * es;
+    d.f32 = sg.f32;
+  }
+  return d;
+}
+__device__ __forceinline__ void f8_store_column(const F8Column& d, int c0, int n, const float* v) {
+  if (!d.p) return;
+  uint8_t* p = d.p + (long long)c0 * d.pitch;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (j < n) {
+      if (d.f32) *reinterpret_cast<float*>(p) = v[j];
+      else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v[j]);
+    }
+    p += d.pitch;
+  }
 }
 
-template <int BN, int kStages>
+// The general store of rows, out of line: it is long and rarely runs.
+__device__ __noinline__ void f8_store_general(const GemmOut& out, int M, int N, int r, int c0, int n, int acc_addr) {
+  float v[32];
+  sm100::tmem_ld_32x32b_x32(acc_addr, v);
+  if (r < M) store_chunk32<__nv_bfloat16>(out, r, c0, min(N, c0 + n), v);
+}
+
+template <int BN, int kGroups>
 __global__ void __launch_bounds__(kF8GemmThreads, 1)
     gemm_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, F8GemmArgs a) {
-  using Cfg = F8GemmCfg<BN, kStages>;
+  using Cfg = F8GemmCfg<BN, kGroups>;
+  constexpr int kStages = Cfg::kStages;
   using namespace sm100;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -218,61 +254,74 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {  // ---------------- TMA producer
-      int stage = 0;
+      int grp = 0;
       uint32_t phase = 0;
       for (int unit = blockIdx.x; unit < total && !*abort_flag; unit += gridDim.x) {
         const int tile = unit / g.k_split, kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
         int mt, nt;
         gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1)) { *abort_flag = 1; break; }
-          mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
-          tma_load_2d(&tmA, &full[stage], smA + stage * Cfg::A_BYTES, kb * Cfg::BK, mt * Cfg::BM);
-          tma_load_2d(&tmB, &full[stage], smB + stage * Cfg::B_BYTES, kb * Cfg::BK, nt * BN);
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        for (int kb = kb0; kb < kb1; kb += 4) {   // a group; blocks past the end pass through empty
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int stage = 4 * grp + i;
+            if (!mbar_wait(&empty[stage], phase ^ 1)) { *abort_flag = 1; kb = kb1; break; }
+            if (kb + i < kb1) {
+              mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
+              tma_load_2d(&tmA, &full[stage], smA + stage * Cfg::A_BYTES, (kb + i) * Cfg::BK, mt * Cfg::BM);
+              tma_load_2d(&tmB, &full[stage], smB + stage * Cfg::B_BYTES, (kb + i) * Cfg::BK, nt * BN);
+            } else {
+              mbar_arrive(&full[stage]);
+            }
+          }
+          if (++grp == kGroups) { grp = 0; phase ^= 1; }
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---------------- MMA issuer
-      // One thread's instructions set the pace (an MMA takes BN / 2 cycles), so
-      // a group of four K blocks is unrolled: the scale bytes' place in their
-      // cells is a constant, descriptors and barriers advance by one add.
+      // One thread's instructions set the pace: an MMA takes BN / 2 cycles of
+      // the tensor pipe, and four of them with a wait, a commit and the ring's
+      // bookkeeping took this thread 480 cycles and a group's copies of scales
+      // another 420.  So the scale warp copies the scales, a group of four K
+      // blocks is unrolled over constant stages and constant places of the
+      // scale bytes (418 cycles a block), only the descriptors' low words
+      // change, and barriers are looked at ahead of the MMAs before them.
       constexpr uint32_t idesc = idesc_mxe4m3(Cfg::BM, BN, 0);
-      const uint64_t ad0 = sdesc_k_sw128(smem_u32(smA)), bd0 = sdesc_k_sw128(smem_u32(smB));
-      const uint32_t full0 = smem_u32(full), sf_full0 = smem_u32(sf_full), sf_smem0 = smem_u32(smSf);
-      int stage = 0, acc = 0, sb = 0;
+      const uint32_t a_lo0 = sdesc_lo(smem_u32(smA), 16), b_lo0 = sdesc_lo(smem_u32(smB), 16);
+      const uint32_t full0 = smem_u32(full), sf_full0 = smem_u32(sf_full);
+      int grp = 0, acc = 0, sb = 0;
       uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
       bool ok = true;
       for (int unit = blockIdx.x; unit < total && ok && !*abort_flag; unit += gridDim.x) {
-        const int kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
+        const int kb0 = g.k_split == 1 ? 0 : (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
         if (!mbar_wait_small(smem_u32(&tempty[acc]), acc_phase ^ 1)) { ok = false; break; }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
         for (int kb = kb0; ok && kb < kb1; kb += 4) {
           const uint32_t sf_tmem = tmem_base + (uint32_t)(2 * BN + sb * Cfg::SF_COLS);
+          const uint32_t full_g = full0 + 32u * (uint32_t)grp;
+          const uint32_t a_lo = a_lo0 + (uint32_t)(grp * (4 * Cfg::A_BYTES >> 4)),
+                         b_lo = b_lo0 + (uint32_t)(grp * (4 * Cfg::B_BYTES >> 4));
+          uint32_t ready = mbar_test(full_g, phase);
           if (!mbar_wait_small(sf_full0 + 8u * (uint32_t)sb, sf_phase)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 1 + Cfg::SFB_GROUPS; ++i)
-            tmem_cp_scales(sf_tmem + 4u * (uint32_t)i, sf_smem0 + (uint32_t)(sb * Cfg::SF_BYTES + 512 * i));
-#pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (kb + i < kb1) {
-              if (!mbar_wait_small(full0 + 8u * (uint32_t)stage, phase)) { ok = false; break; }
+            if (!ready && !mbar_wait_small(full_g + 8u * i, phase)) ok = false;
+            if (i < 3) ready = mbar_test(full_g + 8u * (i + 1), phase);
+            if (ok && kb + i < kb1) {
               tc_fence_after();
-              const uint64_t ad = desc_add(ad0, stage * Cfg::A_BYTES), bd = desc_add(bd0, stage * Cfg::B_BYTES);
 #pragma unroll
               for (int k = 0; k < Cfg::BK / 32; ++k)
-                mma_mxf8(d_tmem, desc_add(ad, k * 32), desc_add(bd, k * 32),
+                mma_mxf8(d_tmem, a_lo + (uint32_t)(i * (Cfg::A_BYTES >> 4) + 2 * k),
+                         b_lo + (uint32_t)(i * (Cfg::B_BYTES >> 4) + 2 * k), sdesc_hi(1024),
                          idesc | ((uint32_t)i << 4) | ((uint32_t)i << 29), (kb != kb0 || i != 0 || k != 0) ? 1u : 0u,
                          sf_tmem, sf_tmem + 4u);
-              mma_commit(&empty[stage]);
-              if (++stage == kStages) { stage = 0; phase ^= 1; }
             }
+            mma_commit(&empty[4 * grp + i]);
           }
           mma_commit(&sf_empty[sb]);
           if (++sb == Cfg::kSfBufs) { sb = 0; sf_phase ^= 1; }
+          if (++grp == kGroups) { grp = 0; phase ^= 1; }
         }
         mma_commit(&tfull[acc]);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -282,8 +331,9 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
   } else if (warp >= 3) {  // ---------------- epilogue warps 3..10
     const int sub = warp & 3;                  // TMEM lane quarter this warp may access
     const int e = warp - 3;
-    constexpr int kCols = BN / 2;              // this warp's columns
-    const int col0 = (e >> 2) * kCols;
+    constexpr int kHalf = (BN / 2 + 31) / 32 * 32;   // columns of the first four warps; the others take the rest
+    const int col0 = (e >> 2) * kHalf, cols = e < 4 ? kHalf : BN - kHalf;
+    const bool by_column = g.transpose_out || g.k_split > 1;
     uint8_t* stage_out = smOut + e * (32 * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -292,22 +342,26 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
       int mt, nt;
       gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
       const int c0 = nt * BN + col0;
-      const F8Dest d = f8_dest(g, mt * Cfg::BM + 32 * sub, c0, kCols);
+      const F8Dest d = f8_dest(g, mt * Cfg::BM + 32 * sub, c0, cols);
+      F8Column fc;
+      if (by_column) fc = f8_column(g, m_tiles, mt * Cfg::BM + 32 * sub + lane, ks);
       if (!mbar_wait(&tfull[acc], acc_phase)) { *abort_flag = 1; break; }
       tc_fence_after();
       __syncwarp();
       const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + (uint32_t)(acc * BN + col0);
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
-        if (!d.p) {
-          if (c0 + c < g.N) f8_store_general(g, m_tiles, mt, sub, ks, c0 + c, (int)(ta + c), stage_out);
+      for (int c = 0; c < d.cols; c += 32) {   // (a last half step reads 16 columns too many, all of them allocated)
+        if (!d.p && !by_column) {
+          f8_store_general(g.out, g.M, g.N, mt * Cfg::BM + 32 * sub + lane, c0 + c, d.cols - c, (int)(ta + c));
           continue;
         }
         float v[32];
         tmem_ld_32x32b_x32(ta + (uint32_t)c, v);
-        if (d.f32) {
-          f8_store_rows(d, 4 * c, reinterpret_cast<const uint4*>(v), stage_out);
-          f8_store_rows(d, 4 * c + 64, reinterpret_cast<const uint4*>(v + 16), stage_out);
+        if (by_column) {
+          f8_store_column(fc, c0 + c, d.cols - c, v);
+        } else if (d.f32) {
+          f8_store_rows(d, 4 * c, 4 * (d.cols - c), reinterpret_cast<const uint4*>(v), stage_out);
+          f8_store_rows(d, 4 * c + 64, 4 * (d.cols - c) - 64, reinterpret_cast<const uint4*>(v + 16), stage_out);
         } else {
           uint32_t w[16];
 #pragma unroll
@@ -315,7 +369,7 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
             w[j] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          f8_store_rows(d, 2 * c, reinterpret_cast<const uint4*>(w), stage_out);
+          f8_store_rows(d, 2 * c, 2 * (d.cols - c), reinterpret_cast<const uint4*>(w), stage_out);
         }
       }
       tc_fence_before();
@@ -354,7 +408,15 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
           dst[32 * (1 + j)] = make_uint4(wb[4 * j], wb[4 * j + 1], wb[4 * j + 2], wb[4 * j + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_full[sb]);
+        if (lane == 0) {   // to TMEM; sf_full completes with the copies
+          tc_fence_after();
+          const uint32_t sf_tmem = tmem_base + (uint32_t)(2 * BN + sb * Cfg::SF_COLS);
+          const uint32_t sf_smem = smem_u32(smSf + sb * Cfg::SF_BYTES);
+#pragma unroll
+          for (int i = 0; i < 1 + Cfg::SFB_GROUPS; ++i) tmem_cp_scales(sf_tmem + 4u * (uint32_t)i, sf_smem + 512u * i);
+          mma_commit(&sf_full[sb]);
+        }
+        __syncwarp();
         if (++sb == Cfg::kSfBufs) { sb = 0; sf_phase ^= 1; }
       }
       if (!ok) {

@@ -430,8 +430,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
   } else if (warp == 9) {
     // ------------------------------------------------------------ S issuer
     constexpr uint32_t idS = idesc_e4m3_f32(128, kPart);
-    const uint64_t qd0 = sdesc_k_sw128(smem_u32(sm));
-    const uint64_t cd0 = sdesc_k_sw128(smem_u32(sm + kOffC));
+    const uint32_t qd0 = sdesc_lo(smem_u32(sm), 16), cd0 = sdesc_lo(smem_u32(sm + kOffC), 16);
     uint32_t g = 0, qw = 0, n = 0;   // parts, items with parts, items
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
@@ -447,13 +446,14 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         fence_proxy_async_smem();
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t cd = desc_add(cd0, st * kPart * 128);
+          const uint32_t cd = cd0 + (uint32_t)(st * kPart * 128 >> 4);
 #pragma unroll
           for (int kc = 0; kc < 4; ++kc)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_f8(tmem + kColS + (uint32_t)(kPart * st), desc_add(qd0, kc * kQChunk + ks * 32),
-                     desc_add(cd, kc * kChunk + ks * 32), idS, (kc | ks) != 0 ? 1u : 0u);
+              mma_f8(tmem + kColS + (uint32_t)(kPart * st), qd0 + (uint32_t)((kc * kQChunk + ks * 32) >> 4),
+                     cd + (uint32_t)((kc * kChunk + ks * 32) >> 4), sdesc_hi(1024), sdesc_hi(1024), idS,
+                     (kc | ks) != 0 ? 1u : 0u);
           mma_commit(&s_full[st]);
           if (j == np - 1) mma_commit(q_empty);
         }
@@ -469,8 +469,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
     // ------------------------------------------------------------ O issuer
     constexpr uint32_t idHi = idesc_e4m3_f32(64, 256) | (1u << 16);   // B is MN-major
     constexpr uint32_t idLo = idHi | (1u << 7);                       // A is E5M2
-    const uint64_t vd0 = sdesc_mn_sw128(smem_u32(sm + kOffC), kChunk, 1024);
-    const uint64_t pd0 = sdesc_k_sw128(smem_u32(sm + kOffP));
+    const uint32_t vd0 = sdesc_lo(smem_u32(sm + kOffC), kChunk), pd0 = sdesc_lo(smem_u32(sm + kOffP), 16);
     uint32_t g = 0, oi = 0, n = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
@@ -484,16 +483,16 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         if (!warp_wait_small(&p_full[st], (g / kParts) & 1)) { ok = false; break; }
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t pd = desc_add(pd0, st * kPBytes), vd = desc_add(vd0, st * kPart * 128);
+          const uint32_t pd = pd0 + (uint32_t)(st * kPBytes >> 4), vd = vd0 + (uint32_t)(st * kPart * 128 >> 4);
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh)
-                mma_f8(tmem + ((uint32_t)(16 * hh) << 16) + kColO, desc_add(pd, 64 * hl + 32 * ks),
-                       desc_add(vd, 2 * hh * kChunk + 32 * ks * 128), hl ? idLo : idHi,
-                       (j > 0 || ks > 0 || hl > 0) ? 1u : 0u);
+                mma_f8(tmem + ((uint32_t)(16 * hh) << 16) + kColO, pd + (uint32_t)((64 * hl + 32 * ks) >> 4),
+                       vd + (uint32_t)((2 * hh * kChunk + 32 * ks * 128) >> 4), sdesc_hi(1024), sdesc_hi(1024),
+                       hl ? idLo : idHi, (j > 0 || ks > 0 || hl > 0) ? 1u : 0u);
           mma_commit(&t_done[st]);
         }
         __syncwarp();
