@@ -1618,7 +1618,8 @@ bool mqa_f8_tc_ok(const csa_dims* d) {
 int mqa_f8_splits(const csa_dims* d, int rows, int* parts_per_split) {
   const int parts = (d->topk + mqaf8::kPart - 1) / mqaf8::kPart;
   const long long items = (long long)rows * (d->nh / mqaf8::kHeads);
-  const int n = items > 0 ? (int)std::min<long long>(parts, std::max(1ll, sm_count() / items)) : 1;
+  int n = items > 0 ? (int)std::min<long long>(parts, std::max(1ll, sm_count() / items)) : 1;
+  n = std::min(n, mqaf8::kMaxSplits);
   *parts_per_split = (parts + n - 1) / n;
   return (parts + *parts_per_split - 1) / *parts_per_split;
 }

@@ -85,6 +85,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr int kItems = 4;                         // item descriptors in flight
 constexpr int kReaders = 4 + 4 + 3 + 8;           // warps that read each of them
 constexpr int kThreads = 640;
+constexpr int kMaxSplits = 64;                    // of a (row, head group)
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 // w <= 2^(kOff + kGrow) = 362 < 448: the running maximum may lag by kGrow, and
 // the largest weight stays above 2^kOff.  A rescale of O costs a part's time
@@ -734,12 +735,12 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
       tc_fence_after();
       const float lsum = grp == 0 ? lm + lother : lother + lm;   // the same sum in both groups
       const float inv = lsum == 0.f ? 0.f : exp2f(-kOff) / lsum;
-      // O / l in four passes of 32 columns per lane.  bf16 rows go through 32 staging rows of 64 bytes (row = lane:
-      // head 16 sub + lane % 16, channels 256 (lane / 16) + 128 grp + 32 p ..) that alias this quarter's rows of P
-      // buffer grp, which only this warp writes.
+      // O / l in four passes of 32 columns per lane, through 32 staging rows (row = lane: head 16 sub + lane % 16,
+      // channels 256 (lane / 16) + 128 grp + 32 p ..) that alias this quarter's rows of the P buffers grp and
+      // grp + 2, which only this warp writes: 64 bytes a row in bf16, 128 bytes in fp32 (a split's partial output).
       uint8_t* stage = sm + kOffP + grp * kPBytes + 16 * sub * 128;
       __nv_bfloat16* ob = a.O + (long long)w.row * a.ld_O + (long long)(w.hg * kHeads + 16 * sub) * kC + 128 * grp;
-      float* po = a.part_o + (((long long)w.row * a.nh + head) * a.splits + w.split) * kC + 256 * half + 128 * grp;
+      float* po = a.part_o + (((long long)w.row * a.nh + w.hg * kHeads + 16 * sub) * a.splits + w.split) * kC + 128 * grp;
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         float v[32];
@@ -750,10 +751,19 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
           if (lane == 0) mbar_arrive(o_free);
         }
         if (a.splits > 1) {
-          float4* o = reinterpret_cast<float4*>(po + 32 * p);
+          auto row = [&](int r) { return stage + (r >> 4) * (2 * kPBytes); };
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            o[q] = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4*>(row(lane) + sw128(lane & 15, u)) =
+                make_float4(v[4 * u] * inv, v[4 * u + 1] * inv, v[4 * u + 2] * inv, v[4 * u + 3] * inv);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), u = lane & 7;
+            const float4 val = *reinterpret_cast<const float4*>(row(r) + sw128(r & 15, u));
+            *reinterpret_cast<float4*>(po + (long long)(r & 15) * a.splits * kC + 256 * (r >> 4) + 32 * p + 4 * u) = val;
+          }
+          __syncwarp();
           continue;
         }
 #pragma unroll
@@ -787,25 +797,49 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
 
 // Joins the splits of a (row, head): O = sum_i o_i 2^(lse_i) / sum_i 2^(lse_i),
 // the splits added in order.  One CTA of 128 threads per (row, head), four
-// channels per thread.
+// channels per thread.  The work is all memory latency (32 splits of 2 KB), so
+// the weights are read by lanes of a warp at once and eight splits' values are
+// in flight.
 __global__ void __launch_bounds__(128) mqa_f8_join_kernel(const float* part_o, const float* part_lse, int nh, int splits,
                                                           __nv_bfloat16* O, long long ld_O) {
+  __shared__ float w_s[mqaf8::kMaxSplits];
   pdl_prologue_done();
   const long long rh = blockIdx.x;
-  const float* lse = part_lse + rh * splits;
-  float top = -INFINITY;
-  for (int i = 0; i < splits; ++i) top = fmaxf(top, lse[i]);
+  const int lane = threadIdx.x & 31;
+  const float4* o = reinterpret_cast<const float4*>(part_o + rh * splits * mqaf8::kC) + threadIdx.x;
+  float lse[mqaf8::kMaxSplits / 32], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < mqaf8::kMaxSplits / 32; ++i) {
+    lse[i] = 32 * i + lane < splits ? part_lse[rh * splits + 32 * i + lane] : -INFINITY;
+    top = fmaxf(top, lse[i]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int i = 0; i < mqaf8::kMaxSplits / 32; ++i)   // 0 where nothing was seen (and part_o was not written)
+      w_s[32 * i + lane] = lse[i] == -INFINITY ? 0.f : exp2f(lse[i] - top);
+  }
+  __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int i = 0; i < splits; ++i) {
-    if (lse[i] == -INFINITY) continue;   // nothing seen: part_o was not written
-    const float w = exp2f(lse[i] - top);
-    const float4 o = reinterpret_cast<const float4*>(part_o + (rh * splits + i) * mqaf8::kC)[threadIdx.x];
-    sum += w;
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+  for (int i0 = 0; i0 < splits; i0 += 8) {
+    float4 v[8];
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = i0 + i < splits ? w_s[i0 + i] : 0.f;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (w[i] != 0.f) v[i] = o[(long long)(i0 + i) * (mqaf8::kC / 4)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum += w[i];
+      acc.x = fmaf(w[i], v[i].x, acc.x);
+      acc.y = fmaf(w[i], v[i].y, acc.y);
+      acc.z = fmaf(w[i], v[i].z, acc.z);
+      acc.w = fmaf(w[i], v[i].w, acc.w);
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const long long row = rh / nh;
