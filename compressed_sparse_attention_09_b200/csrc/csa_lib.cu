@@ -1463,6 +1463,8 @@ csa_status csa_decode_q8_staged(const csa_dims* d, const void* packed, const voi
 // ====================================================================== block-scaled E4M3 rows
 namespace {
 
+constexpr int kMaxF8Width = 1 << 28;   // columns are counted in 32 bits, a warp's steps past the row's end included
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // How the row kernels walk over rows row0 .. n - 1 of w values (f8::Walk), as
@@ -1713,7 +1715,7 @@ csa_status csa_quantize_f8(int dtype, const void* X, long long ld, int n, int w,
   if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
   if (!X || !codes || !scales || n < 0 || w <= 0 || ld < w || ld_codes < w || (slots && n_slots < 0))
     return CSA_ERR_INVALID_ARG;
-  if (block != 0 && block != f8::kBlock) return CSA_ERR_UNSUPPORTED;
+  if ((block != 0 && block != f8::kBlock) || w > kMaxF8Width) return CSA_ERR_UNSUPPORTED;
   if (ld_scales < (block ? (w + block - 1) / block : 1)) return CSA_ERR_INVALID_ARG;
   const int v = dtype == CSA_BF16 ? 8 : 4;
   if (w % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(X) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
@@ -1729,7 +1731,7 @@ csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, c
   if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
   if (!X || !codes || !scales || n < 0 || w <= 0 || ld < w || ld_codes < w || n_slots < 0 || (!rows && n > n_slots))
     return CSA_ERR_INVALID_ARG;
-  if (block != 0 && block != f8::kBlock) return CSA_ERR_UNSUPPORTED;
+  if ((block != 0 && block != f8::kBlock) || w > kMaxF8Width) return CSA_ERR_UNSUPPORTED;
   if (ld_scales < (block ? (w + block - 1) / block : 1)) return CSA_ERR_INVALID_ARG;
   const int v = dtype == CSA_BF16 ? 8 : 4;
   if (w % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(X) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
@@ -1757,7 +1759,8 @@ csa_status csa_quantize_weight_f8(int dtype, const void* W, long long ld, int N,
       ld_scales < (K + f8::kBlock - 1) / f8::kBlock)
     return CSA_ERR_INVALID_ARG;
   const int v = dtype == CSA_BF16 ? 8 : 4;
-  if (K % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(W) || !aligned16(codes)) return CSA_ERR_UNSUPPORTED;
+  if (K % f8::kUnit || K > kMaxF8Width || ld % v || ld_codes % 16 || !aligned16(W) || !aligned16(codes))
+    return CSA_ERR_UNSUPPORTED;
   return launch_quantize_squares(dtype, W, ld, N, K, codes, ld_codes, scales, ld_scales, (cudaStream_t)stream);
 }
 

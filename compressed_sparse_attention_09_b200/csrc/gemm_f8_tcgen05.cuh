@@ -96,8 +96,9 @@ __device__ __forceinline__ uint32_t r_sw64(int r, int u) { return (uint32_t)(r *
 // must be short: the destination is worked out once per tile, and where the
 // tile's columns lie in one segment with 16-byte aligned rows, a step is 32
 // columns through the warp's staging rows (row = lane) and out as 64-byte
-// pieces of rows.  Anything else (a ragged
-// edge, an odd row stride, several segments) takes the general store.
+// pieces of rows.  The transposed and split forms go down columns
+// (F8Column); anything else (an odd row stride, an edge that is no whole
+// piece, several segments) takes the general store.
 struct F8Dest {
   uint8_t* p;      // row 0 of this warp's 32, column 0 of its range; NULL: general store
   long long pitch; // bytes between rows
@@ -254,8 +255,9 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {  // ---------------- TMA producer
-      int grp = 0;
+      int grp = 0, round = 0;   // round: passes over the ring
       uint32_t phase = 0;
+      int issued = 0;           // stages filled in this round
       for (int unit = blockIdx.x; unit < total && !*abort_flag; unit += gridDim.x) {
         const int tile = unit / g.k_split, kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
         int mt, nt;
@@ -265,6 +267,7 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const int stage = 4 * grp + i;
             if (!mbar_wait(&empty[stage], phase ^ 1)) { *abort_flag = 1; kb = kb1; break; }
+            issued = stage + 1;
             if (kb + i < kb1) {
               mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
               tma_load_2d(&tmA, &full[stage], smA + stage * Cfg::A_BYTES, (kb + i) * Cfg::BK, mt * Cfg::BM);
@@ -273,7 +276,18 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
               mbar_arrive(&full[stage]);
             }
           }
-          if (++grp == kGroups) { grp = 0; phase ^= 1; }
+          if (++grp == kGroups) {
+            grp = 0;
+            phase ^= 1;
+            ++round;
+            issued = 0;
+          }
+        }
+      }
+      if (*abort_flag) {   // a wait ran out somewhere: no load may outlive the CTA's shared memory
+        for (int s = 0; s < kStages; ++s) {
+          const int last = s < issued ? round : round - 1;   // the stage's last fill
+          if (last >= 0) mbar_wait_small(smem_u32(&full[s]), (uint32_t)last & 1u);
         }
       }
     }

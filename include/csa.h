@@ -19,10 +19,10 @@
  *    may start its on-chip set-up while the previous kernel on the stream
  *    finishes, but it waits for that kernel to complete before it reads or
  *    writes any memory, so the order of all memory effects is the stream
- *    order.  The one exception is inside csa_decode / csa_decode_q8: the
- *    cache append runs beside the c^Q-side projection of the same call,
- *    whose buffers (workspace rows, packed weights) it does not touch; the
- *    call as a whole keeps the stream order.
+ *    order.  The one exception is inside csa_decode / csa_decode_q8 /
+ *    csa_decode_f8: the cache append runs beside the c^Q-side projection of
+ *    the same call, whose buffers (workspace rows, packed weights) it does
+ *    not touch; the call as a whole keeps the stream order.
  *  - Matrices are dense row-major.  "ld" arguments are row strides in
  *    ELEMENTS.  Element type = csa_dims.dtype for activations and weights
  *    (fp32 or bf16); the indexer head weights w^I are always fp32 and block
@@ -473,8 +473,8 @@ csa_status csa_decode_q8_staged(const csa_dims* dims, const void* packed, const 
  *                     the same slot leave that slot's contents undefined.
  * n_slots           : destination rows (used with slots only).
  * codes, scales [dev]: destination, row strides ld_codes, ld_scales (bytes).
- * Requires w, ld_codes multiples of 16, rows of X and codes 16-byte aligned
- * (CSA_ERR_UNSUPPORTED). */
+ * Requires w <= 2^28, w and ld_codes multiples of 16, rows of X and codes
+ * 16-byte aligned (CSA_ERR_UNSUPPORTED). */
 csa_status csa_quantize_f8(int dtype, const void* X, long long ld, int n, int w, int block, const int* slots,
                            int n_slots, void* codes, long long ld_codes, void* scales, long long ld_scales,
                            void* stream);

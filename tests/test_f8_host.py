@@ -72,7 +72,7 @@ def launches(f):
     (dict(dtype=5), INVALID), (dict(X=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
     (dict(n=-1), INVALID), (dict(w=0), INVALID), (dict(ld=504), INVALID), (dict(ld_codes=504), INVALID),
     (dict(block=128, ld_scales=3), INVALID), (dict(ld_scales=0), INVALID), (dict(slots=P, n_slots=-1), INVALID),
-    (dict(block=64), UNSUPPORTED), (dict(w=504), UNSUPPORTED), (dict(ld=516), UNSUPPORTED),
+    (dict(block=64), UNSUPPORTED), (dict(w=504), UNSUPPORTED), (dict(w=(1 << 28) + 16, ld=1 << 30, ld_codes=1 << 30), UNSUPPORTED), (dict(ld=516), UNSUPPORTED),
     (dict(ld_codes=520), UNSUPPORTED), (dict(X=ODD), UNSUPPORTED), (dict(codes=ODD), UNSUPPORTED), (dict(n=0), OK)])
 def test_quantize_refusals(change, status):
     a = dict(dtype=csa.CSA_BF16, X=P, ld=512, n=4, w=512, block=0, slots=None, n_slots=0, codes=P, ld_codes=512, scales=P,
