@@ -43,8 +43,8 @@
 // its lower 16 lanes, their lo rows in the upper 16.
 //
 // Warps (20): 0-3 gather codes (16-byte cp.async, one entry per warp and
-// instruction); 4-7 split q, a lane quarter each; 8 fetches the entries'
-// scales; 9 issues S, 10 issues O (one thread each); 11 owns TMEM and posts
+// instruction) and split half of q; 4-7 split the other half; 8 fetches the
+// entries' scales; 9 issues S, 10 issues O (one thread each); 11 owns TMEM and posts
 // the work items ahead of their consumers; 12-19 softmax and epilogue.
 // Every wait is bounded (sm100::mbar_wait); the groups meet on mbarriers,
 // never on a named barrier, so a wait that ran out cannot strand a partner.
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
   if (warp < 4) {
     // ------------------------------------------------------------ gather (warps 0-3)
     // entry warp + 4 i of a part per instruction, a lane 16 bytes; slots fetched one part ahead
-    uint32_t g = 0, n = 0;   // ring parts, items
+    uint32_t g = 0, qw = 0, n = 0;   // ring parts, items with parts, items
     bool ok = true;
     const uint32_t ring = smem_u32(sm + kOffC + (lane >> 3) * kChunk);
     const uint32_t swz0 = sw128(warp, lane & 7), swz1 = sw128(warp + 4, lane & 7);
@@ -344,8 +344,16 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
       MqaF8Item w;
       if (!item_of(n++, w)) break;
       if (w.p0 >= w.p1) continue;
-      const long long n_ent = rowmap_entries(a.rm, a.rows);
       const int* ir = a.idx + (long long)w.row * a.topk;
+      if (qw++ > 0) {   // their share of q (see the q warps)
+        const __nv_bfloat16* q64 = a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads) * kC;
+        if (!mqa_f8_split_q(q64, 32 + 8 * warp, 8, sm, qs_s, q_empty, qw & 1)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          mbar_arrive(q_full);
+        }
+      }
+      const long long n_ent = rowmap_entries(a.rm, a.rows);
       auto slot = [&](int p) {
         const int e = p * kPart + warp + 4 * lane;
         return lane < 16 && e < a.topk ? __ldg(ir + e) : -1;
@@ -373,8 +381,9 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
     cp_async_wait_all();
   } else if (warp < 8) {
     // ------------------------------------------------------------ q split (warps 4-7)
-    // 16 heads each; of the first item 4 each, the softmax warps taking the
-    // other 48 (they have nothing else to do yet)
+    // 8 heads each, the gather warps taking the other 32 (the next item's S
+    // waits for q, so its first entries can wait too); of the first item 4
+    // each, the softmax warps taking 48 (they have nothing else to do yet)
     uint32_t qw = 0, n = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
       if (warp_aborted(abort_flag)) break;
@@ -383,13 +392,13 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
       if (w.p0 >= w.p1) continue;
       const __nv_bfloat16* q64 = a.q + (long long)w.row * a.ld_q + (long long)(w.hg * kHeads) * kC;
       const bool first = qw == 0;
-      const int heads = first ? 4 : 16;
+      const int heads = first ? 4 : 8;
       if (!mqa_f8_split_q(q64, (warp - 4) * heads, heads, sm, qs_s, q_empty, (qw & 1) ^ 1)) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
       if (lane == 0)
-        for (int u = 0; u < (first ? 1 : 4); ++u) mbar_arrive(q_full);
+        for (int u = 0; u < (first ? 1 : 2); ++u) mbar_arrive(q_full);
       ++qw;
     }
   } else if (warp == 8) {
