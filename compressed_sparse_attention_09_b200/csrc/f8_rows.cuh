@@ -182,8 +182,9 @@ __device__ __forceinline__ bool walk_start(const Walk& w, int& row, int& col) {
 // Blocks of 128: a warp step is 32 vectors of a row (two blocks of bf16, one
 // of fp32), so that a block never crosses a step; a warp takes kSteps steps.
 // Bound by issue slots before HBM when each step looked up its own row (147
-// instructions a step, 23 us for 8192 x 4096 bf16 against 15 us of traffic);
-// hence the constant strides and the packed arithmetic.
+// instructions a step, 23.9 us for 8192 x 4096 bf16 against 15.4 us of
+// traffic); hence the constant strides, the packed arithmetic and a path of its
+// own for infinite values (20.7 us, 4.9 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
   constexpr int V = Vec<T>::V, kStep = 32 * V;
@@ -229,7 +230,8 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
   }
 }
 
-// One scale for the whole row: one warp per row.  Rows of up to kSteps steps
+// One scale for the whole row: one warp per row (32768 rows of 512 bf16 to
+// scattered slots: 10.5 us, 4.8 TB/s).  Rows of up to kSteps steps
 // (1024 bf16, 512 fp32 values) stay in registers; longer ones are read twice
 // (the second time from L2).
 template <typename T>
@@ -338,6 +340,8 @@ struct DequantArgs {
 };
 
 // Read back: a warp step is 32 output vectors of a row; a warp takes kSteps.
+// 131072 rows of 512 to fp32: 55.8 us, 6.0 TB/s (with a thread per 16 codes,
+// whose stores covered half of each sector at a time, 73 us).
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs a) {
   constexpr int V = Vec<T>::V, kStep = 32 * V;

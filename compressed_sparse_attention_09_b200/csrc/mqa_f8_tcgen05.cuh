@@ -31,11 +31,14 @@
 // channels = N, two chunks apart by the ring's length).
 //
 // What bounds it is the chain gather -> S -> softmax -> O -> free of a part
-// (the MMAs take 16 x 48 + 8 x 128 = 1.8 K cycles of it), so the ring holds
-// four parts, each with its own S and P buffer, and two groups of four softmax
-// warps take alternate parts: while one waits on TMEM, shared memory or the
-// other's M, the other computes.  (128-entry parts, whose S runs at the full
-// MMA rate, with both groups on one part: 7 K cycles per 128 entries.)
+// (the MMAs take 16 x 48 + 8 x 128 = 1.8 K cycles of it, the gather 2.3 K
+// beside their shared-memory reads), so the ring holds four parts, each with
+// its own S and P buffer, and two groups of four softmax warps take alternate
+// parts: while one waits on TMEM, shared memory or the other's M, the other
+// computes.  A part takes 2.6 K cycles.  64 decode rows of 128 heads and 2048
+// entries run in 61.6 us (both groups on one 128-entry tile: 67.7; S over
+// pairs of parts: 68.3; eight warps that gather and split q: 71.2), 8192
+// packed rows of 64 heads and up to 512 entries in 752 us.
 //
 // TMEM (512 columns): O in columns 0-255 (channels 0-255 in the lower 16
 // lanes of every lane quarter, 256-511 in the upper 16); four S buffers of 64
