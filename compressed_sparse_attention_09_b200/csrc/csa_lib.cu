@@ -1467,21 +1467,18 @@ constexpr int kMaxF8Width = 1 << 28;   // columns are counted in 32 bits, a warp
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// How the row kernels walk over rows row0 .. n - 1 of w values (f8::Walk), as
-// many of them as 32-bit warp numbers allow; the next launch starts at next.
-f8::Walk f8_walk(int dtype, int w, int row0, int n, int* next) {
+// How the row kernels walk over n rows of w values (f8::Walk).  A warp takes at
+// least 64 of them, so rows that fit any memory give warp numbers of 31 bits.
+f8::Walk f8_walk(int dtype, int w, int n) {
   const int step = 32 * (dtype == CSA_BF16 ? 8 : 4), per = (w + step - 1) / step;
   f8::Walk k;
   const bool along = per >= f8::kSteps;   // kSteps steps of one row, or one step of kSteps rows
   k.cols = along ? (per + f8::kSteps - 1) / f8::kSteps : per;
   k.row_step = along ? 0 : 1;
   k.col_step = along ? 1 : 0;
-  const long long most = (1ll << 30) / k.cols * (along ? 1 : f8::kSteps);
-  k.row0 = row0;
-  k.n = (int)std::min<long long>(n, row0 + most);
-  const long long rows = k.n - row0, groups = along ? rows : (rows + f8::kSteps - 1) / f8::kSteps;
-  k.warps = (unsigned)(groups * k.cols);
-  *next = k.n;
+  k.n = n;
+  k.warps = (unsigned)std::min<long long>((along ? (long long)n : ((long long)n + f8::kSteps - 1) / f8::kSteps) * k.cols,
+                                          0x7FFFFFFF);
   return k;
 }
 
@@ -1497,14 +1494,12 @@ csa_status launch_quantize(int dtype, f8::QuantArgs a, int block, cudaStream_t s
     CSA_CHECK_LAUNCH();
     return CSA_OK;
   }
-  for (int r = 0; r < a.n;) {
-    a.walk = f8_walk(dtype, a.w, r, a.n, &r);
-    const dim3 grid((a.walk.warps + 7) / 8);
-    const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, grid, dim3(256), 0, st, a)
-                            : launch_pdl(f8::quantize_blocks_kernel<float>, grid, dim3(256), 0, st, a);
-    if (e != cudaSuccess) return CSA_ERR_CUDA;
-    CSA_CHECK_LAUNCH();
-  }
+  a.walk = f8_walk(dtype, a.w, a.n);
+  const dim3 grid((a.walk.warps + 7) / 8);
+  const cudaError_t e = b ? launch_pdl(f8::quantize_blocks_kernel<bf16>, grid, dim3(256), 0, st, a)
+                          : launch_pdl(f8::quantize_blocks_kernel<float>, grid, dim3(256), 0, st, a);
+  if (e != cudaSuccess) return CSA_ERR_CUDA;
+  CSA_CHECK_LAUNCH();
   return CSA_OK;
 }
 
@@ -1740,15 +1735,13 @@ csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, c
   a.codes = static_cast<const uint8_t*>(codes); a.ld_codes = ld_codes; a.scales = static_cast<const uint8_t*>(scales);
   a.ld_scales = ld_scales; a.rows = rows; a.n_slots = n_slots; a.X = X; a.ld = ld; a.w = w;
   a.block = block ? block : w;
-  for (int r = 0; r < n;) {
-    a.walk = f8_walk(dtype, w, r, n, &r);
-    const dim3 grid((a.walk.warps + 7) / 8);
-    const cudaError_t e =
-        dtype == CSA_BF16 ? launch_pdl(f8::dequantize_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, a)
-                          : launch_pdl(f8::dequantize_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, a);
-    if (e != cudaSuccess) return CSA_ERR_CUDA;
-    CSA_CHECK_LAUNCH();
-  }
+  a.walk = f8_walk(dtype, w, n);
+  const dim3 grid((a.walk.warps + 7) / 8);
+  const cudaError_t e =
+      dtype == CSA_BF16 ? launch_pdl(f8::dequantize_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, a)
+                        : launch_pdl(f8::dequantize_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, a);
+  if (e != cudaSuccess) return CSA_ERR_CUDA;
+  CSA_CHECK_LAUNCH();
   return CSA_OK;
 }
 

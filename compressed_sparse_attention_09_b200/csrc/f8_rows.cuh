@@ -145,9 +145,8 @@ template <typename T> struct Vec {
 // Work is numbered warp by warp, `cols` warps to a row (or group of rows).
 struct Walk {
   int cols, row_step, col_step;   // col_step in steps
-  unsigned warps;                 // of this launch
-  int row0;                       // its first row
-  int n;                          // end of its rows
+  unsigned warps;
+  int n;                          // rows
 };
 
 struct QuantArgs {
@@ -174,7 +173,7 @@ __device__ __forceinline__ bool walk_start(const Walk& w, int& row, int& col) {
   const unsigned i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (i >= w.warps) return false;
   const unsigned r = i / (unsigned)w.cols, c = i - r * (unsigned)w.cols;
-  row = w.row0 + (int)r * (w.row_step ? kSteps : 1);
+  row = (int)r * (w.row_step ? kSteps : 1);
   col = ((int)c * (w.row_step ? 1 : kSteps) * 32 + (int)(threadIdx.x & 31)) * V;
   return true;
 }

@@ -108,8 +108,10 @@ __device__ __forceinline__ int mqa_f8_nparts(const int* ir, int topk, int avail)
       v[u] = j < topk ? __ldg(ir + j) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < 16; ++u)
+    for (int u = 0; u < 16; ++u) {
       if (v[u] >= 0 && v[u] < avail) last = j0 + 32 * u + lane;
+      else if (v[u] != -1) flag_status(kStatusBadIndex);   // (those before the last valid slot: the scale warp too)
+    }
     last = __reduce_max_sync(0xffffffffu, last);
     if (last >= 0) return last / mqaf8::kPart + 1;
   }

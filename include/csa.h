@@ -520,7 +520,9 @@ size_t csa_mqa_f8_workspace_bytes(const csa_dims* dims, int rows);
  * scales [total_blocks] (block = 0) replace Ccomp; everything else is as
  * there.  q and O are of dims.dtype, 16-byte aligned, and q's row stride a
  * multiple of 16 bytes (CSA_ERR_UNSUPPORTED).  A row whose slots are all -1
- * gives zeros.
+ * gives zeros; the rows are those of the sequences (cu_seqlens[nseq] =
+ * total_tokens).  A NaN among a selected entry's codes or scales, or in a
+ * head's query, gives NaN in the rows or the head it belongs to.
  * ws [dev]: >= csa_mqa_f8_workspace_bytes(dims, total_tokens), 256-byte
  *           aligned; may be NULL where that is 0.  Calls that overlap need
  *           their own. */

@@ -233,7 +233,7 @@ def tc_dims(nh, k, m=4):
 
 @pytest.mark.parametrize("B,nh,k,cap", [(1, 64, 1, 5), (1, 64, 64, 80), (2, 64, 128, 200), (3, 128, 129, 300),
                                         (1, 128, 300, 310), (5, 64, 257, 700), (1, 128, 2048, 2500), (80, 128, 130, 140),
-                                        (160, 64, 65, 90)])
+                                        (160, 64, 65, 90), (2, 192, 70, 100), (1, 192, 8192, 8300)])
 def test_decode_mqa_tensor_cores(B, nh, k, cap):
     rng = np.random.default_rng(k + B)
     dims = tc_dims(nh, k)
@@ -295,6 +295,58 @@ def test_decode_mqa_bad_index_is_flagged_and_skipped():
     q, codes, scales, out = decode_mqa(dims, 2, 60, avail, idx, 14)
     assert csa.csa_get_device_status() == 5
     check_rows(dims, q, codes, scales, idx, [0, 60], avail, out)
+
+
+def test_decode_mqa_bad_index_after_the_last_valid_slot_is_flagged():
+    """Also where no part of the row is worked on: slots beyond the last valid one, and a row that sees nothing."""
+    rng = np.random.default_rng(22)
+    dims = tc_dims(64, 700)
+    for avail, slot in ([60, 60], 650), ([60, 0], 3):
+        idx = picked(rng, 2, 700, avail)
+        idx[1, slot] = 60
+        q, codes, scales, out = decode_mqa(dims, 2, 60, avail, idx, 23)
+        assert csa.csa_get_device_status() == 5
+        check_rows(dims, q, codes, scales, idx, [0, 60], avail, out)
+
+
+@pytest.mark.parametrize("m", [1, 2, 8])
+def test_decode_mqa_other_block_lengths(m):
+    rng = np.random.default_rng(m)
+    dims = tc_dims(64, 90, m)
+    avail = [120, 0, 77]
+    idx = picked(rng, 3, 90, avail)
+    q, codes, scales, out = decode_mqa(dims, 3, 120, avail, idx, 24)
+    assert csa.csa_get_device_status() == 0
+    check_rows(dims, q, codes, scales, idx, [0, 120, 240], avail, out)
+
+
+def test_decode_mqa_nan_stays_where_it_belongs():
+    """NaN in one head's query, an infinite query value, NaN among one row's selected entries: NaN there, the other heads
+    and rows right, the rows that the same CTA takes next among them."""
+    rng = np.random.default_rng(25)
+    B, cap = 300, 70
+    dims = tc_dims(64, 66)
+    idx = picked(rng, B, 66, [cap] * B)
+    codes, scales = entries(rng, B * cap, 512)
+    q = torch.as_tensor(rng.standard_normal((B, 64 * 512)), dtype=F32).to(BF16).to(DEV)
+    q[299, 3 * 512 + 7] = float("nan")
+    q[299, 5 * 512] = float("inf")
+    q[298, 9 * 512 + 500] = float("-inf")
+    codes[297 * cap + int(idx[297, 65]), 100] = 0x7F
+    scales[296 * cap + int(idx[296, 0])] = 255
+    q, codes, scales, out = decode_mqa(dims, B, cap, [cap] * B, idx, 26, codes=codes, scales=scales, q=q)
+    assert csa.csa_get_device_status() == 0
+    o = out.view(B, 64, 512)
+    assert torch.isnan(o[299, [3, 5]]).all() and torch.isnan(o[298, 9]).all() and torch.isnan(o[296:298]).all()
+    ok = torch.ones(B, 64, dtype=torch.bool)
+    ok[299, [3, 5]] = ok[298, 9] = False
+    ok[296:298] = False
+    assert torch.isfinite(o[ok.to(DEV)]).all()
+    check_rows(dims, q, codes, scales, idx, [b * cap for b in range(B)], [cap] * B, out, [0, 1, 148, 150, 151, 152, 295])
+    for r in (298, 299):
+        heads = ok[r].nonzero()[:, 0].to(DEV)
+        want, bound = ref.mqa(q[r].double().view(64, 512)[heads], codes, scales, r * cap + idx[r].long().to(DEV), BF16)
+        assert ((o[r][heads].double() - want).abs() <= bound).all()
 
 
 def test_decode_mqa_unselected_rows_are_never_read():
