@@ -93,6 +93,8 @@ def run_all():
     rows_case(21, 272, 128, 2, "blocks", out)
     gemm_case(5, 200, 1024, torch.float32, 3, "gemm_few", out)
     gemm_case(200, 300, 400, torch.bfloat16, 4, "gemm_many", out)
+    gemm_case(131, 301, 400, torch.bfloat16, 8, "gemm_odd", out)
+    gemm_case(131, 301, 400, torch.float32, 9, "gemm_odd_f32", out)
     decode_case(TC, B=1, pos0=2045, cap=640, steps=5, seed=5, name="decode_1", out=out)
     decode_case(TC, B=6, pos0=30, cap=40, steps=3, seed=6, name="decode_6", out=out)
     prefill_case(TC, [90, 1, 57], 7, "prefill", out)

@@ -141,7 +141,7 @@ def test_quantize_weight_bit_for_bit(N, K, dtype):
 
 
 # ---------------------------------------------------------------- product
-def gemm_case(M, N, K, dtype, seed, spread=6, pad=0):
+def gemm_case(M, N, K, dtype, seed, spread=6, pad=0, shift=0):
     g = torch.Generator().manual_seed(seed)
     lda, ldd = -(-K // 16) * 16 + 16 * pad, N + pad
     kb, nb = -(-K // 128), -(-N // 128)
@@ -151,7 +151,8 @@ def gemm_case(M, N, K, dtype, seed, spread=6, pad=0):
     b[(b & 127) == 127] = 5
     sa = torch.randint(127 - spread, 128 + spread, (M, kb + pad), generator=g).to(torch.uint8)
     sb = torch.randint(127 - spread, 128 + spread, (nb, kb + pad), generator=g).to(torch.uint8)
-    out = torch.full((M, ldd), 5.0, dtype=dtype, device=DEV)
+    whole = torch.full((M * ldd + shift,), 5.0, dtype=dtype, device=DEV)   # the output begins `shift` values in
+    out = whole[shift:].view(M, ldd)
     ws = torch.empty(csa.csa_gemm_f8_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV)
     a, b, sa, sb = (t.to(DEV) for t in (a, b, sa, sb))
     csa.csa_gemm_f8(KIND[dtype], a, lda, sa, kb + pad, b, lda, sb, kb + pad, M, N, K, out, ldd, ws)
@@ -161,7 +162,7 @@ def gemm_case(M, N, K, dtype, seed, spread=6, pad=0):
     held = torch.isfinite(bound)
     assert held.float().mean() > 0.5
     assert (err[held] <= bound[held]).all(), (float((err / bound)[held].max()), M, N, K)
-    assert (out[:, N:] == 5).all()
+    assert (out[:, N:] == 5).all() and (whole[:shift] == 5).all()
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (3, 200, 512), (64, 257, 640), (64, 4160, 4096), (17, 100, 16),
@@ -181,6 +182,13 @@ def test_gemm_many_rows(M, N, K, dtype):
 @pytest.mark.parametrize("M", [5, 150])
 def test_gemm_strides_and_extreme_scales(M):
     gemm_case(M, 330, 700, F32, 1, spread=60, pad=3)
+
+
+@pytest.mark.parametrize("M,N,K,pad,shift", [(301, 481, 144, 1, 0), (130, 480, 256, 0, 1), (200, 720, 128, 3, 5),
+                                             (97, 239, 400, 0, 3), (256, 241, 128, 7, 0)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_outputs_off_the_16_byte_grid(M, N, K, pad, shift, dtype):
+    gemm_case(M, N, K, dtype, M + N + K, pad=pad, shift=shift)
 
 
 # ---------------------------------------------------------------- attention
