@@ -23,7 +23,7 @@
 // with R a lane's running maximum of s and M the head's (lagging) running
 // maximum of s + log2(scale_e), so that the weights use E4M3's range whatever
 // the entries' scales are.  The normaliser is summed in fp32 from the
-// unrounded probabilities.
+// unrounded probabilities, relative to the maximum of s alone.
 //
 // The codes sit in shared memory once, [4 chunks of 128 channels][256 ring
 // entries][128 bytes] in the 128-byte swizzle: S reads 64 entries as a
@@ -80,8 +80,8 @@ constexpr int kPBytes = 64 * 128;                 // P of a part: 64 heads x (64
 constexpr int kOffC = 4 * kQChunk;
 constexpr int kOffP = kOffC + 4 * kChunk;         // kParts P buffers; the epilogue's staging rows between items
 constexpr int kOffE = kOffP + kParts * kPBytes;   // scale (fp32) of each ring entry
-constexpr int kOffX = kOffE + kParts * kPart * 4; // xch: [2 groups][64 heads] fp32
-constexpr int kOffS = kOffX + 2 * kHeads * 4;     // q scale of each head
+constexpr int kOffX = kOffE + kParts * kPart * 4; // xch: [2 groups][64 heads] pairs of fp32
+constexpr int kOffS = kOffX + 2 * kHeads * 8;     // q scale of each head
 constexpr int kOffMisc = kOffS + kHeads * 4;
 constexpr size_t kSmem = kOffMisc + 768;          // the swizzled tiles need a base aligned to 1024 bytes
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
     return;
   }
   float* e_s = reinterpret_cast<float*>(sm + kOffE);
-  float* xch = reinterpret_cast<float*>(sm + kOffX);
+  float2* xch = reinterpret_cast<float2*>(sm + kOffX);
   float* qs_s = reinterpret_cast<float*>(sm + kOffS);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + kOffMisc);
   uint64_t* q_empty = q_full + 1;         // the item's last S done, and every softmax warp has its q scales
@@ -575,12 +575,12 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
     uint32_t seen_n = 0;                // values of the other group's warp read so far
     // Values go from a group's warp to the other group's warp of the same
     // lane quarter and come back in turn, so one slot each is enough.
-    auto post = [&](float v) {
-      if (half == 0) xch[grp * kHeads + hrow] = v;
+    auto post = [&](float v, float u) {
+      if (half == 0) xch[grp * kHeads + hrow] = make_float2(v, u);
       __syncwarp();
       if (lane == 0) mbar_arrive(&x_bar[4 * grp + sub]);
     };
-    auto receive = [&](float& v) {
+    auto receive = [&](float2& v) {
       const bool ok = warp_wait_small(&x_bar[4 * (grp ^ 1) + sub], seen_n & 1);
       ++seen_n;
       v = xch[(grp ^ 1) * kHeads + hrow];
@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
       const uint64_t qs2 = pk2(qs, qs);
       float R = -INFINITY, l = 0.f;    // this lane's running maximum of s, and its sum of 2^(s - R)
       float M = -INFINITY;             // the head's (lagging) maximum of s + log2(scale)
+      float2 seen;                     // what the other group posted
       const int np = w.p1 - w.p0;
       const uint32_t glast = g + (uint32_t)np - 1;
       for (int j = (int)((g ^ (uint32_t)grp) & 1); ok && j < np; j += 2) {
@@ -694,10 +695,13 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         }
         float tmax = Ru + lg2_approx_f32(umax);   // log2(0) = -inf
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 16));
-        if (j > 0 && !receive(M)) { ok = false; break; }   // M after the part before
+        if (j > 0) {   // M after the part before
+          if (!receive(seen)) { ok = false; break; }
+          M = seen.x;
+        }
         const bool grow = tmax > M + kGrow;   // also on the first part with a valid entry
         const float Mn = grow ? tmax : M;
-        post(Mn);
+        post(Mn, 0.f);
         if (__any_sync(kFull, grow && j > 0)) {   // rescale O: its earlier products must have completed
           const uint32_t gp = gj - 1;
           if (!warp_wait_small(&t_done[gp % kParts], (gp / kParts) & 1)) { ok = false; break; }
@@ -733,22 +737,30 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[st]);
       }
-      // the head's M is that of the item's last part; its normaliser, relative to M, is the sum of both groups'
+      // The head's M is that of the item's last part.  Its normaliser is that of all its lanes' (R, l), relative to
+      // the largest R: M says nothing of it, as an entry's score and its scale are independent (a zero entry has the
+      // score 0 and the scale 2^-127).
       const bool last_mine = (int)(glast & 1) == grp;
-      if (ok && !last_mine) ok = receive(M);
-      float lm = l > 0.f && M != -INFINITY ? l * ex2_approx_f32(fminf(R - M, 126.f)) : l;
-      lm += __shfl_xor_sync(kFull, lm, 16);
-      float lother = 0.f;
-      if (ok && !last_mine) post(lm);
-      if (ok) ok = receive(lother);
-      if (ok && last_mine) post(lm);
+      if (ok && !last_mine) {
+        ok = receive(seen);
+        M = seen.x;
+      }
+      const float Rh = fmaxf(R, __shfl_xor_sync(kFull, R, 16));
+      float lh = l * ex2_approx_f32(R - (Rh == -INFINITY ? 0.f : Rh));
+      lh += __shfl_xor_sync(kFull, lh, 16);
+      seen = make_float2(-INFINITY, 0.f);
+      if (ok && !last_mine) post(Rh, lh);
+      if (ok) ok = receive(seen);
+      if (ok && last_mine) post(Rh, lh);
       if (!ok || !warp_wait_small(&t_done[glast % kParts], (glast / kParts) & 1)) {
         if (lane == 0) *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const float lsum = grp == 0 ? lm + lother : lother + lm;   // the same sum in both groups
-      const float inv = lsum == 0.f ? 0.f : exp2f(-kOff) / lsum;
+      const float top = fmaxf(Rh, seen.x), ref = top == -INFINITY ? 0.f : top;
+      const float lmine = lh * ex2_approx_f32(Rh - ref), lother = seen.y * ex2_approx_f32(seen.x - ref);
+      const float lsum = grp == 0 ? lmine + lother : lother + lmine;   // the same sum in both groups
+      const float inv = lsum == 0.f ? 0.f : exp2f(M - ref - kOff) / lsum;   // O holds sums of 2^(s - M + kOff) scale code
       // O / l in four passes of 32 columns per lane, through 32 staging rows (row = lane: head 16 sub + lane % 16,
       // channels 256 (lane / 16) + 128 grp + 32 p ..) that alias this quarter's rows of the P buffers grp and
       // grp + 2, which only this warp writes: 64 bytes a row in bf16, 128 bytes in fp32 (a split's partial output).
@@ -797,7 +809,8 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         __syncwarp();
       }
       if (a.splits > 1 && grp == 0 && half == 0)
-        a.part_lse[((long long)w.row * a.nh + head) * a.splits + w.split] = lsum == 0.f ? -INFINITY : M + log2f(lsum);
+        a.part_lse[((long long)w.row * a.nh + head) * a.splits + w.split] =
+            lsum == 0.f ? -INFINITY : ref + log2f(lsum);   // 0: no valid entry
       g += (uint32_t)np;
     }
   }
