@@ -94,6 +94,11 @@ constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 // the largest weight stays above 2^kOff.  A rescale of O costs a part's time
 // (it waits for the products in flight), so kGrow is most of E4M3's range.
 constexpr float kOff = 3.5f, kGrow = 5.f;
+// M counts no scale below this, so that M >= R - 123 for every maximum R of the
+// scores and 2^(R - M + kOff) <= 2^126.5 is in fp32's range.  Where all of a
+// head's scales are smaller its largest weight is 2^(-127 + 118 + kOff) = 2^-5.5
+// or more, which hi still holds as a normal number.
+constexpr float kMinScale = 0x1p-118f;
 }  // namespace mqaf8
 
 // Parts of 64 slots up to the row's last valid slot (0 <= s < avail), by a
@@ -179,6 +184,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// 2^x like ex2_approx_f32, with subnormal results.
+__device__ __forceinline__ float ex2_approx_all_f32(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float lg2_approx_f32(float x) {
   float y;
@@ -693,7 +704,7 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
           const float2 ls = upk2(l2);
           l = ls.x + ls.y;
         }
-        float tmax = Ru + lg2_approx_f32(umax);   // log2(0) = -inf
+        float tmax = Rn + lg2_approx_f32(fmaxf(umax, kMinScale));   // -inf while this lane has seen nothing
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 16));
         if (j > 0) {   // M after the part before
           if (!receive(seen)) { ok = false; break; }
@@ -722,7 +733,9 @@ __global__ void __launch_bounds__(mqaf8::kThreads, 1) mqa_f8_tc_kernel(MqaF8TcAr
         M = Mn;
         // w = u 2^(R - M + kOff), as hi + lo.  The part's P buffer is free: its S could only be issued on ring
         // entries that the O product of four parts before, the buffer's last reader, had released.
-        const float f = ex2_approx_f32(fminf(Ru - (M == -INFINITY ? 0.f : M) + kOff, 126.f));
+        // (f is as small as 2^-123 times the lane's part of the softmax where scales are large: subnormal, with u above
+        // one.  The bound on f is for lanes that have seen nothing, whose u is 0.)
+        const float f = ex2_approx_all_f32(fminf(Ru - (M == -INFINITY ? 0.f : M) + kOff, 127.f));
         const uint64_t f2 = pk2(f, f);
         uint32_t hi[8], lo[8];
 #pragma unroll
