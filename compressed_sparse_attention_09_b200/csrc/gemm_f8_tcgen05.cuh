@@ -36,6 +36,7 @@
 // short of the power limit), 1001 x 4160 x 4096 in 23.8 us, 64 rows of 73728 x
 // 1536 weights in 25.8 us (4.8 TB/s).
 #pragma once
+#include "f8_ring.h"
 #include "gemm_tcgen05.cuh"
 
 namespace csa {
@@ -288,41 +289,29 @@ __global__ void __launch_bounds__(kF8GemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {  // ---------------- TMA producer
-      int grp = 0, round = 0;   // round: passes over the ring
-      uint32_t phase = 0;
-      int issued = 0;           // stages filled in this round
-      for (int unit = blockIdx.x; unit < total && !*abort_flag; unit += gridDim.x) {
-        const int tile = unit / g.k_split, kb0 = (unit % g.k_split) * kbs, kb1 = min(k_blocks, kb0 + kbs);
-        int mt, nt;
-        gemm_tile_coords(tile, m_tiles, n_tiles, g.group_m, mt, nt);
-        for (int kb = kb0; kb < kb1; kb += 4) {   // a group; blocks past the end pass through empty
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int stage = 4 * grp + i;
-            if (!mbar_wait(&empty[stage], phase ^ 1)) { *abort_flag = 1; kb = kb1; break; }
-            issued = stage + 1;
-            if (kb + i < kb1) {
-              mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
-              tma_load_2d(&tmA, &full[stage], smA + stage * Cfg::A_BYTES, (kb + i) * Cfg::BK, mt * Cfg::BM);
-              tma_load_2d(&tmB, &full[stage], smB + stage * Cfg::B_BYTES, (kb + i) * Cfg::BK, nt * BN);
-            } else {
-              mbar_arrive(&full[stage]);
-            }
+      struct {
+        const CUtensorMap *tmA, *tmB;
+        const TcGemmArgs& g;
+        uint64_t *full, *empty;
+        uint8_t *smA, *smB;
+        volatile int* abort_flag;
+        int m_tiles, n_tiles, mt, nt;
+        __device__ __forceinline__ bool aborted() const { return *abort_flag != 0; }
+        __device__ __forceinline__ void abort() { *abort_flag = 1; }
+        __device__ __forceinline__ void tile(int t) { gemm_tile_coords(t, m_tiles, n_tiles, g.group_m, mt, nt); }
+        __device__ __forceinline__ bool wait_empty(int s, uint32_t parity) { return mbar_wait(&empty[s], parity); }
+        __device__ __forceinline__ void fill(int s, int kb, bool real) {
+          if (!real) {
+            mbar_arrive(&full[s]);
+            return;
           }
-          if (++grp == kGroups) {
-            grp = 0;
-            phase ^= 1;
-            ++round;
-            issued = 0;
-          }
+          mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+          tma_load_2d(tmA, &full[s], smA + s * Cfg::A_BYTES, kb * Cfg::BK, mt * Cfg::BM);
+          tma_load_2d(tmB, &full[s], smB + s * Cfg::B_BYTES, kb * Cfg::BK, nt * BN);
         }
-      }
-      if (*abort_flag) {   // a wait ran out somewhere: no load may outlive the CTA's shared memory
-        for (int s = 0; s < kStages; ++s) {
-          const int last = s < issued ? round : round - 1;   // the stage's last fill
-          if (last >= 0) mbar_wait_small(smem_u32(&full[s]), (uint32_t)last & 1u);
-        }
-      }
+        __device__ __forceinline__ void wait_full(int s, uint32_t parity) { mbar_wait_small(smem_u32(&full[s]), parity); }
+      } ops{&tmA, &tmB, g, full, empty, smA, smB, abort_flag, m_tiles, n_tiles, 0, 0};
+      f8_fill_ring<kGroups>(ops, (int)blockIdx.x, total, (int)gridDim.x, g.k_split, kbs, k_blocks);
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---------------- MMA issuer
