@@ -1463,7 +1463,11 @@ csa_status csa_decode_q8_staged(const csa_dims* d, const void* packed, const voi
 // ====================================================================== block-scaled E4M3 rows
 namespace {
 
-constexpr int kMaxF8Width = 1 << 28;   // columns are counted in 32 bits, a warp's steps past the row's end included
+// Rows and columns are counted in 32 bits, a warp's steps past a row's end, a
+// tile's past the last row and a grid's past the last square included.
+constexpr int kMaxF8Width = 1 << 28, kMaxF8Rows = 1 << 30;
+// Whether the products' and the weight quantiser's sizes are in that range.
+bool f8_sizes_ok(int M, int N, int K) { return M <= kMaxF8Rows && N <= kMaxF8Rows && K <= kMaxF8Width; }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -1752,13 +1756,13 @@ csa_status csa_quantize_weight_f8(int dtype, const void* W, long long ld, int N,
       ld_scales < (K + f8::kBlock - 1) / f8::kBlock)
     return CSA_ERR_INVALID_ARG;
   const int v = dtype == CSA_BF16 ? 8 : 4;
-  if (K % f8::kUnit || K > kMaxF8Width || ld % v || ld_codes % 16 || !aligned16(W) || !aligned16(codes))
+  if (!f8_sizes_ok(0, N, K) || K % f8::kUnit || ld % v || ld_codes % 16 || !aligned16(W) || !aligned16(codes))
     return CSA_ERR_UNSUPPORTED;
   return launch_quantize_squares(dtype, W, ld, N, K, codes, ld_codes, scales, ld_scales, (cudaStream_t)stream);
 }
 
 size_t csa_gemm_f8_workspace_bytes(int M, int N, int K) {
-  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || !f8_sizes_ok(M, N, K)) return 0;
   return align_up(f8_gemm_ws(M, N, K));
 }
 
@@ -1767,6 +1771,7 @@ csa_status csa_gemm_f8(int out_dtype, const void* A, long long lda, const void* 
                        void* ws, size_t ws_bytes, void* stream) {
   if (out_dtype != CSA_F32 && out_dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
   if (!A || !sA || !B || !sB || !D || M < 0 || N <= 0 || K <= 0) return CSA_ERR_INVALID_ARG;
+  if (!f8_sizes_ok(M, N, K)) return CSA_ERR_UNSUPPORTED;
   const int kb = (K + f8::kBlock - 1) / f8::kBlock;
   if (lda < K || ldb < K || ldd < N || ld_sA < kb || ld_sB < kb) return CSA_ERR_INVALID_ARG;
   if (lda % 16 || ldb % 16 || !aligned16(A) || !aligned16(B)) return CSA_ERR_UNSUPPORTED;

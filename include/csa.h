@@ -489,11 +489,13 @@ csa_status csa_dequantize_f8(int dtype, const void* codes, long long ld_codes, c
 
 /* Quantises a K-major weight matrix W [N, K] (row stride ld) with one scale
  * byte for each 128 x 128 values (edges shorter): codes [N, ld_codes], scales
- * [ceil(N / 128), ld_scales].  Alignment as for csa_quantize_f8 (K for w). */
+ * [ceil(N / 128), ld_scales].  Alignment and width as for csa_quantize_f8 (K for
+ * w); N <= 2^30 (CSA_ERR_UNSUPPORTED). */
 csa_status csa_quantize_weight_f8(int dtype, const void* W, long long ld, int N, int K, void* codes,
                                   long long ld_codes, void* scales, long long ld_scales, void* stream);
 
-/* Workspace bytes of csa_gemm_f8 (0 where it needs none). */
+/* Workspace bytes of csa_gemm_f8 (0 where it needs none, and for sizes that it
+ * refuses). */
 size_t csa_gemm_f8_workspace_bytes(int M, int N, int K);
 
 /* D[M, N] = A . B^T of two block-scaled matrices, accumulated in fp32 and
@@ -504,8 +506,8 @@ size_t csa_gemm_f8_workspace_bytes(int M, int N, int K);
  * B [dev] : [N, K] codes, row stride ldb; sB [ceil(N / 128), ld_sB]
  *           (csa_quantize_weight_f8).
  * D [dev] : row stride ldd (elements).
- * Any M >= 0, N, K >= 1; lda and ldb multiples of 16 and A, B 16-byte aligned
- * (CSA_ERR_UNSUPPORTED).
+ * 0 <= M <= 2^30, 1 <= N <= 2^30, 1 <= K <= 2^28; lda and ldb multiples of 16
+ * and A, B 16-byte aligned (CSA_ERR_UNSUPPORTED).
  * ws [dev]: >= csa_gemm_f8_workspace_bytes(M, N, K), 256-byte aligned; may be
  *           NULL where that is 0.  Calls that overlap need their own. */
 csa_status csa_gemm_f8(int out_dtype, const void* A, long long lda, const void* sA, long long ld_sA, const void* B,
