@@ -1544,12 +1544,18 @@ csa_status launch_f8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const F8
   return CSA_OK;
 }
 
-// K slices of a product with few rows (weights as the 128-row operand): as
-// many as fill the SMs, each a multiple of four K blocks (one group of scales).
+// K slices of a product with few rows (weights as the 128-row operand): eight
+// or four equal ones, each a multiple of four K blocks (one group of scales),
+// where they have an SM each and the depth pays for the second launch and the
+// partial sums.  64 rows, in us (unsliced in parentheses): four slices 4160 x
+// 4096 10.0 (11.7), 4160 x 6144 12.0 (16.0), but 4160 x 2048 8.9 (7.7); eight
+// 2304 x 4096 9.9 (11.5), 300 x 8192 8.5 (19.1); two never: 9472 x 1024 10.5
+// (6.8), x 4096 17.1 (13.1), x 8192 23.2 (21.5).  Depths that do not divide run
+// unsliced (4160 x 4224: 13.8).
 int f8_gemm_splits(int M, int N, int K) {
-  if (M > 64) return 1;
   const int w_tiles = (N + 127) / 128, k_blocks = (K + 127) / 128;
-  for (int ks = 8; ks >= 2; ks /= 2)
+  if (M > 64 || k_blocks < 32) return 1;
+  for (int ks = 8; ks >= 4; ks /= 2)
     if ((long long)w_tiles * ks <= sm_count() && k_blocks % (4 * ks) == 0) return ks;
   return 1;
 }

@@ -1,5 +1,5 @@
 """What the 8-bit operators answer to sizes near the end of 32 bits, where counts of tiles and squares rounded up would
-wrap around: refused before anything is launched (addresses here are fake)."""
+wrap around: refused before anything is launched (addresses here are fake).  And which products are cut into K slices."""
 import ctypes
 
 import pytest
@@ -39,3 +39,12 @@ def test_weight_quantiser_refuses_rows_that_wrap_around(N):
     n0 = csa.csa_launch_count()
     assert csa.lib().csa_quantize_weight_f8(csa.CSA_BF16, P, 256, N, 256, P, 256, P, 2, None) == UNSUPPORTED
     assert csa.csa_launch_count() == n0
+
+
+@pytest.mark.parametrize("M,N,K,slices", [(64, 4160, 4096, 4), (1, 4160, 4096, 4), (64, 2304, 4096, 8), (64, 300, 8192, 8),
+                                          (64, 9472, 1024, 1), (64, 9472, 8192, 1), (64, 4160, 2048, 1), (5, 1000, 2048, 1),
+                                          (64, 4160, 4224, 1), (65, 4160, 4096, 1)])
+def test_products_are_sliced_where_that_pays(M, N, K, slices):
+    """Deep products in four or eight slices; shallow ones, and wide ones that would get two, are faster whole."""
+    need = slices * -(-N // 128) * 128 * M * 4 if slices > 1 else 0
+    assert csa.csa_gemm_f8_workspace_bytes(M, N, K) == -(-need // 256) * 256

@@ -9,17 +9,18 @@ import compressed_sparse_attention_09_b200 as csa
 import f8_ref as ref
 from compressed_sparse_attention_09_b200 import synth
 from test_gpu_f8 import BF16, DEV, F32, KIND, check_rows, decode_mqa, entries, gemm_case, picked, tc_dims
-from test_gpu_f8_path import state
+from test_gpu_f8_path import gemm_call, state
 from test_gpu_parity import gpu_pack
 
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("M,N,K,slices", [(64, 2304, 4096, 8), (1, 130, 4096, 8), (33, 4000, 2048, 4), (64, 9472, 1024, 2),
-                                          (7, 4865, 4080, 2), (1, 4160, 3968, 1), (64, 4160, 4224, 1),
+@pytest.mark.parametrize("M,N,K,slices", [(64, 2304, 4096, 8), (1, 130, 4096, 8), (33, 4000, 2048, 1), (64, 9472, 1024, 1),
+                                          (33, 4000, 4096, 4), (7, 4500, 8176, 4), (7, 4865, 4080, 1), (1, 4160, 3968, 1), (64, 4160, 4224, 1),
                                           (64, 520, 1536, 1), (5, 520, 2560, 1)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_product_by_slices(M, N, K, slices, dtype):
+    """Eight and four slices (whole blocks at their ends or not) and sizes that are not sliced."""
     need = csa.csa_gemm_f8_workspace_bytes(M, N, K)
     assert need == (0 if slices == 1 else -(-slices * -(-N // 128) * 128 * M * 4 // 256) * 256)
     gemm_case(M, N, K, dtype, M + N + K)
@@ -77,6 +78,40 @@ def test_weights_that_are_not_finite(dtype):
     assert np.array_equal(codes[fin].numpy(), want[fin.numpy()])
     assert ((codes[~fin] & 0x7F) == 0x7F).all()
     assert np.array_equal(scales.cpu().numpy(), ws) and ws[1, 0] == 0 and ws[2, 3] == 0
+
+
+def test_sliced_products_captured_and_on_two_streams():
+    """Two products in slices, each with its own workspace, replayed from graphs and queued on streams of their own."""
+    calls = [gemm_call(7, 300, 4096, 1), gemm_call(64, 4160, 4096, 2)]
+    assert csa.csa_gemm_f8_workspace_bytes(7, 300, 4096) and csa.csa_gemm_f8_workspace_bytes(64, 4160, 4096)
+    want = []
+    for call, v in calls:
+        call()
+        torch.cuda.synchronize()
+        want.append(v["out"].clone())
+        v["out"].zero_()
+    streams = [torch.cuda.Stream() for _ in calls]
+    graphs = []
+    torch.cuda.synchronize()
+    for (call, _), st in zip(calls, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            call()
+        graphs.append(g)
+    for how in "queued", "replayed":
+        for _ in range(5):
+            for (call, _), g, st in zip(calls, graphs, streams):
+                if how == "queued":
+                    call(st)
+                else:
+                    with torch.cuda.stream(st):
+                        g.replay()
+        torch.cuda.synchronize()
+        assert csa.csa_get_device_status() == 0
+        for (_, v), w in zip(calls, want):
+            assert w.abs().sum() > 0 and torch.equal(v["out"], w), how
+            v["out"].zero_()
+        torch.cuda.synchronize()
 
 
 # ---------------------------------------------------------------- the decode step, step behind step
