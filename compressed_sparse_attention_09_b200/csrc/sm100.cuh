@@ -404,7 +404,8 @@ __host__ __device__ constexpr uint32_t idesc_mxe4m3(int M, int N, int sf_id) {
 // Copy 32 rows of 16 bytes (512 contiguous bytes of shared memory) to four
 // TMEM columns, the same 32 lanes' worth in every lane quarter: the scale
 // bytes of 128 operand rows (row 32 j + i in word j of the i-th 16 bytes).
-// Ordered before the MMAs the same thread issues after it.
+// MMAs that another thread issues need an mma_commit after it, and a wait for
+// that commit's barrier.
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
   const uint64_t desc = (uint64_t)((smem_addr >> 4) & 0x3FFFu)   // start address / 16
                         | ((uint64_t)(128 >> 4) << 32)            // 8-row groups 128 B apart
